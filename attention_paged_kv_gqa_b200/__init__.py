@@ -6,4 +6,6 @@ synthetic inputs.
 """
 from .binding import (AttnError, attn_check_device, attn_decode_paged,  # noqa: F401
                       attn_decode_workspace_size, attn_device_error, attn_fwd_dense,
-                      attn_fwd_varlen_paged, MASK_CAUSAL, MASK_NONE, MASK_PATCH)
+                      attn_decode_paged_q4, attn_fwd_varlen_paged, attn_fwd_varlen_paged_q4,
+                      attn_kv_append_paged_q4, attn_kv_append_rope_paged, attn_kv_gather_paged_q4,
+                      attn_rope, MASK_CAUSAL, MASK_NONE, MASK_PATCH)

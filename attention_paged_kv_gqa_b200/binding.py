@@ -86,6 +86,25 @@ def lib():
         L.attn_bwd_varlen.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, F,
                                       I, I, P, Z, P]
         L.attn_bwd_varlen.restype = I
+        L.attn_rope.argtypes = [P] * 8 + [I, I, I, I, P, I, I, P, I, P, I, I, P]
+        L.attn_rope.restype = I
+        append = [P] * 7 + [P, P]                       # q .. v_cache
+        pages = [P, I, I, I]                            # block_table .. block_size
+        rope = [P, I, I, P, I, P, I]                    # cos_sin .. interleaved
+        L.attn_kv_append_rope_paged.argtypes = append + pages + [P, P, P, I, I, I, I, I] + rope + [I, P, P, P, P]
+        L.attn_kv_append_rope_paged.restype = I
+        L.attn_kv_append_paged_q4.argtypes = append + [P, P] + pages + [P, P, P, I, I, I, I, I, I] + rope + [P]
+        L.attn_kv_append_paged_q4.restype = I
+        L.attn_kv_gather_paged_q4.argtypes = [P] * 4 + pages + [P, P, I, I, I, I, I, P, P, P]
+        L.attn_kv_gather_paged_q4.restype = I
+        L.attn_decode_q4_workspace_size.argtypes = [I] * 4
+        L.attn_decode_q4_workspace_size.restype = Z
+        L.attn_decode_paged_q4.argtypes = [P] * 5 + pages + [P, I, I, I, I, I, F, I, F, P, P, P, Z, P]
+        L.attn_decode_paged_q4.restype = I
+        L.attn_fwd_q4_workspace_size.argtypes = [I] * 6
+        L.attn_fwd_q4_workspace_size.restype = Z
+        L.attn_fwd_varlen_paged_q4.argtypes = [P] * 5 + pages + [P, P] + [I] * 8 + [F, I, I, F, P, P, P, Z, P]
+        L.attn_fwd_varlen_paged_q4.restype = I
         _lib = L
     return _lib
 
@@ -479,3 +498,358 @@ def attn_bwd_dense(q, k, v, o, dout, lse, *, causal=False, scale=None, window_le
                                  mask=MASK_CAUSAL if causal else MASK_NONE, scale=scale,
                                  window_left=window_left, stream=stream)
     return dq.reshape(B, Lq, Hq, D), dk.reshape(B, Lk, Hkv, D), dv.reshape(B, Lk, Hkv, D)
+
+
+# ---------------------------------------------------------------- rotary positions, 4-bit cache
+# These calls check their tensors (type, shape, layout, device) before the pointers
+# leave for C, and run on the tensors' device whichever device is current.
+
+def _need(ok, where, what):
+    if not ok:
+        raise ValueError("%s: %s" % (where, what))
+
+
+def _tensor(t, dtype, shape, dev, where, name, contiguous=True):
+    """t is a tensor of this type and shape (None: any extent) on this device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a tensor" % (where, name))
+    if t.dtype != dtype:
+        raise TypeError("%s: %s must be %s, got %s" % (where, name, dtype, t.dtype))
+    s = t.shape
+    if len(s) != len(shape) or any(b is not None and a != b for a, b in zip(s, shape)):
+        raise ValueError("%s: %s must have shape %s, got %s" % (where, name, tuple(shape), tuple(s)))
+    if t.device != dev:
+        raise ValueError("%s: %s is on %s, not on %s" % (where, name, t.device, dev))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s: %s must be contiguous" % (where, name))
+
+
+def _heads(t, H, D, total, dev, where, name):
+    """A bf16 [total, H, D] view with contiguous heads; returns its (token, head) strides."""
+    _tensor(t, torch.bfloat16, (total, H, D), dev, where, name, contiguous=False)
+    st = t.stride()
+    if st[2] != 1 or st[0] % 8 or st[1] % 8 or t.data_ptr() % 16:
+        raise ValueError("%s: %s needs a contiguous head_dim, strides that are multiples of 8 and a "
+                         "16-byte aligned start" % (where, name))
+    return (ctypes.c_int64 * 2)(st[0], st[1])
+
+
+class _on:
+    """Makes `dev` current for a call, and gives its stream."""
+
+    __slots__ = ("dev", "guard")
+
+    def __init__(self, dev):
+        self.dev = dev
+        self.guard = None
+
+    def __enter__(self):
+        if self.dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def stream(self, stream):
+        return (torch.cuda.current_stream(self.dev) if stream is None else stream).cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cuda(t, where, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a tensor" % (where, name))
+    if t.dim() != 3:
+        raise ValueError("%s: %s must have three dimensions" % (where, name))
+    if t.device.type != "cuda":
+        raise ValueError("%s: %s must be a CUDA tensor" % (where, name))
+    return t.device
+
+
+def _rope_args(cos_sin, positions, pair_axis, total, dev, where, optional):
+    """(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis) as the C calls take them."""
+    if cos_sin is None:
+        _need(optional, where, "cos_sin is required")
+        _need(positions is None and pair_axis is None, where, "positions and pair_axis need cos_sin")
+        return None, 0, 0, None, 1, None
+    _tensor(cos_sin, torch.float32, (None, None), dev, where, "cos_sin")
+    rows, rot = cos_sin.shape
+    axes = 1
+    if positions is None:
+        _need(optional, where, "positions is required")
+    elif positions.dim() == 1:
+        _tensor(positions, torch.int32, (total,), dev, where, "positions")
+    else:
+        _tensor(positions, torch.int32, (None, total), dev, where, "positions")
+        axes = positions.shape[0]
+    if pair_axis is not None:
+        _tensor(pair_axis, torch.int32, (rot // 2,), dev, where, "pair_axis")
+    _need(axes == 1 or pair_axis is not None, where, "several axes need pair_axis")
+    return _at(cos_sin), rows, rot, _at(positions), axes, _at(pair_axis)
+
+
+def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=False, inverse=False,
+              out_q=None, out_k=None, stream=None):
+    """Rotates q [total, Hq, D] and k [total, Hkv, D] (bf16, strided views allowed) by their
+    positions -> (q_out, k_out); k None gives (q_out, None).
+
+    cos_sin: fp32 [max_position, rot_dim], cosines then sines; positions: int32 [total], or
+    [n_axes, total] with pair_axis int32 [rot_dim / 2] naming each pair's axis.  interleaved
+    pairs columns (2 i, 2 i + 1) in place of (i, i + rot_dim / 2).  inverse turns the other
+    way: the gradient of the forward rotation.  out_q / out_k may be q / k themselves.
+    """
+    where = "attn_rope"
+    dev = _cuda(q, where, "q")
+    total, Hq, D = q.shape
+    sq = _heads(q, Hq, D, total, dev, where, "q")
+    rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, False)
+    if out_q is None:
+        out_q = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
+    so = _heads(out_q, Hq, D, total, dev, where, "out_q")
+    Hkv, sk, sko = 0, None, None
+    if k is not None:
+        _cuda(k, where, "k")
+        Hkv = k.shape[1]
+        sk = _heads(k, Hkv, D, total, dev, where, "k")
+        if out_k is None:
+            out_k = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
+        sko = _heads(out_k, Hkv, D, total, dev, where, "out_k")
+    else:
+        _need(out_k is None, where, "out_k without k")
+    if total == 0:
+        return out_q, out_k
+    with _on(dev) as on:
+        st = lib().attn_rope(_at(q), _at(out_q), _at(k), _at(out_k), sq, so, sk, sko, total, Hq, Hkv, D, *rope,
+                             int(bool(interleaved)), int(bool(inverse)), on.stream(stream))
+    _check(st, where)
+    return out_q, out_k
+
+
+def _append_args(q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, q_dtype, where):
+    dev = _cuda(k_new, where, "k_new")
+    total, Hkv, D = k_new.shape
+    sk = _heads(k_new, Hkv, D, total, dev, where, "k_new")
+    sv = _heads(v_new, Hkv, D, total, dev, where, "v_new")
+    Hq, sq = 0, None
+    if q is not None:
+        _cuda(q, where, "q")
+        Hq = q.shape[1]
+        sq = _heads(q, Hq, D, total, dev, where, "q")
+        if out_q is None:
+            out_q = torch.empty((total, Hq, D), dtype=q_dtype, device=dev)
+        _tensor(out_q, q_dtype, (total, Hq, D), dev, where, "out_q")
+        _need(out_q.data_ptr() % 16 == 0, where, "out_q must be 16-byte aligned")
+    else:
+        _need(out_q is None, where, "out_q without q")
+    _tensor(seqused_k, torch.int32, (None,), dev, where, "seqused_k")
+    B = seqused_k.shape[0]
+    _tensor(block_table, torch.int32, (B, None), dev, where, "block_table")
+    if cu_seqlens_new is not None:
+        _tensor(cu_seqlens_new, torch.int32, (B + 1,), dev, where, "cu_seqlens_new")
+    else:
+        _need(total == B, where, "without cu_seqlens_new there is one new token per sequence")
+    if seqused_k_out is None:
+        seqused_k_out = torch.empty_like(seqused_k)
+    _tensor(seqused_k_out, torch.int32, (B,), dev, where, "seqused_k_out")
+    return dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, seqused_k_out
+
+
+def _same_lengths(seqused_k, used, dev, stream):
+    """The lengths after an append of nothing (an empty tensor has no address to pass)."""
+    with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else stream):
+        used.copy_(seqused_k)
+    return used
+
+
+def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, seqused_k, *, cos_sin=None,
+                              positions=None, pair_axis=None, interleaved=False, cu_seqlens_new=None,
+                              descale_q=None, descale_k=None, descale_v=None, out_q=None,
+                              seqused_k_out=None, stream=None):
+    """attn_kv_append_paged with the rotation of q and k (and for an e4m3 cache the
+    quantisation) on the way -> (q_out [total_new, Hq, D] of the cache's type, the new lengths).
+
+    q may be None (q_out is then None).  positions None: each token's position in the cache.
+    """
+    where = "attn_kv_append_rope_paged"
+    fp8 = isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.float8_e4m3fn
+    kind = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, used = _append_args(
+        q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, kind, where)
+    _tensor(k_cache, kind, (None, None, Hkv, D), dev, where, "k_cache")
+    _tensor(v_cache, kind, tuple(k_cache.shape), dev, where, "v_cache")
+    if fp8:
+        for name, d in (("descale_q", descale_q), ("descale_k", descale_k), ("descale_v", descale_v)):
+            if name != "descale_q" or q is not None:
+                _need(isinstance(d, torch.Tensor) and d.numel() == 1, where, name + " must be a one-element tensor")
+                _tensor(d, torch.float32, tuple(d.shape), dev, where, name)
+    rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
+    if total == 0:
+        return out_q, _same_lengths(seqused_k, used, dev, stream)
+    with _on(dev) as on:
+        st = lib().attn_kv_append_rope_paged(
+            _at(q), _at(out_q), _at(k_new), _at(v_new), sq, sk, sv, _at(k_cache), _at(v_cache), _at(block_table),
+            block_table.shape[1], k_cache.shape[0], k_cache.shape[1], _at(cu_seqlens_new), _at(seqused_k), _at(used),
+            B, total, Hq, Hkv, D, *rope, int(bool(interleaved)), FP8_E4M3 if fp8 else BF16,
+            _at(descale_q) if fp8 else None, _at(descale_k) if fp8 else None, _at(descale_v) if fp8 else None,
+            on.stream(stream))
+    _check(st, where)
+    return out_q, used
+
+
+def _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where, Hkv=None, D=None):
+    """Checks a 4-bit cache -> (num_blocks, block_size, Hkv, D, group_size)."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("%s: k_cache must have shape [num_blocks, Hkv, block_size, head_dim / 2]" % where)
+    n, h, bs, half = k_cache.shape
+    _tensor(k_cache, torch.uint8, (n, h if Hkv is None else Hkv, bs, half if D is None else D // 2), dev, where, "k_cache")
+    _tensor(v_cache, torch.uint8, (n, h, bs, half), dev, where, "v_cache")
+    _tensor(k_meta, torch.int16, (n, h, bs, None), dev, where, "k_meta")
+    G = k_meta.shape[3]
+    _tensor(v_meta, torch.int16, (n, h, bs, G), dev, where, "v_meta")
+    _need(G > 0 and 2 * half % G == 0, where, "head_dim must be a multiple of the metas per token")
+    _tensor(block_table, torch.int32, (B, None), dev, where, "block_table")
+    return n, bs, h, 2 * half, 2 * half // G
+
+
+def attn_kv_append_paged_q4(q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, block_table, seqused_k, *,
+                            cos_sin=None, positions=None, pair_axis=None, interleaved=False,
+                            cu_seqlens_new=None, out_q=None, seqused_k_out=None, stream=None):
+    """Appends new tokens to a 4-bit cache, rotating q and k on the way (cos_sin None: no
+    rotation) -> (q_out [total_new, Hq, D] bf16 or None, the new lengths).
+
+    k_cache / v_cache: uint8 [num_blocks, Hkv, 16, D / 2]; k_meta / v_meta: int16
+    [num_blocks, Hkv, 16, D / group_size], group_size 32, 64 or 128 (the format is described
+    in the header).
+    """
+    where = "attn_kv_append_paged_q4"
+    dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, used = _append_args(
+        q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, torch.bfloat16, where)
+    n, bs, _, _, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where, Hkv, D)
+    rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
+    if total == 0:
+        return out_q, _same_lengths(seqused_k, used, dev, stream)
+    with _on(dev) as on:
+        st = lib().attn_kv_append_paged_q4(
+            _at(q), _at(out_q), _at(k_new), _at(v_new), sq, sk, sv, _at(k_cache), _at(v_cache), _at(k_meta),
+            _at(v_meta), _at(block_table), block_table.shape[1], n, bs, _at(cu_seqlens_new), _at(seqused_k), _at(used),
+            B, total, Hq, Hkv, D, gs, *rope, int(bool(interleaved)), on.stream(stream))
+    _check(st, where)
+    return out_q, used
+
+
+def attn_kv_gather_paged_q4(k_cache, v_cache, k_meta, v_meta, block_table, cu_seqlens, total, *, starts=None,
+                            out_k=None, out_v=None, stream=None):
+    """Reads tokens of a 4-bit cache back -> packed (k, v) [total, Hkv, D] bf16, exactly.
+
+    Sequence b's tokens starts[b] .. (None: 0 ..) go to rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
+    """
+    where = "attn_kv_gather_paged_q4"
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.device.type != "cuda":
+        raise ValueError("%s: cu_seqlens must be a CUDA tensor" % where)
+    dev = cu_seqlens.device
+    _tensor(cu_seqlens, torch.int32, (None,), dev, where, "cu_seqlens")
+    B = cu_seqlens.shape[0] - 1
+    _need(B >= 0, where, "cu_seqlens must have B + 1 entries")
+    n, bs, Hkv, D, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
+    if starts is not None:
+        _tensor(starts, torch.int32, (B,), dev, where, "starts")
+    if out_k is None:
+        out_k = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
+    if out_v is None:
+        out_v = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
+    _tensor(out_k, torch.bfloat16, (total, Hkv, D), dev, where, "out_k")
+    _tensor(out_v, torch.bfloat16, (total, Hkv, D), dev, where, "out_v")
+    if total == 0:
+        return out_k, out_v
+    with _on(dev) as on:
+        st = lib().attn_kv_gather_paged_q4(_at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta), _at(block_table),
+                                           block_table.shape[1], n, bs, _at(cu_seqlens), _at(starts), B, int(total),
+                                           Hkv, D, gs, _at(out_k), _at(out_v), on.stream(stream))
+    _check(st, where)
+    return out_k, out_v
+
+
+def attn_decode_q4_workspace_size(B, num_heads_q, num_heads_kv, head_dim) -> int:
+    return int(lib().attn_decode_q4_workspace_size(B, num_heads_q, num_heads_kv, head_dim))
+
+
+def attn_fwd_q4_workspace_size(B, max_seqlen_q, num_heads_q, num_heads_kv, head_dim, total_k) -> int:
+    return int(lib().attn_fwd_q4_workspace_size(B, max_seqlen_q, num_heads_q, num_heads_kv, head_dim, total_k))
+
+
+def _outputs(q, out, lse, lse_shape, return_lse, dev, where):
+    _heads(q, q.shape[1], q.shape[2], q.shape[0], dev, where, "q")
+    _need(q.is_contiguous(), where, "q must be contiguous")
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+    _tensor(out, torch.bfloat16, tuple(q.shape), dev, where, "out")
+    if lse is None and return_lse:
+        lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+    if lse is not None:
+        _tensor(lse, torch.float32, lse_shape, dev, where, "lse")
+    return out, lse
+
+
+def _space(workspace, need, dev, where):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    _tensor(workspace, torch.uint8, (None,), dev, where, "workspace")
+    return workspace
+
+
+def attn_decode_paged_q4(q, k_cache, v_cache, k_meta, v_meta, block_table, seqused_k, *, scale=None,
+                         window_left=-1, softcap=0.0, out=None, lse=None, workspace=None,
+                         return_lse=True, stream=None):
+    """attn_decode_paged over a 4-bit cache: q [B, Hq, D] bf16 -> (o [B, Hq, D] bf16, lse [B, Hq] fp32)."""
+    where = "attn_decode_paged_q4"
+    dev = _cuda(q, where, "q")
+    B, Hq, D = q.shape
+    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
+    _need(Dc == D, where, "q and the cache have different head_dims")
+    _tensor(seqused_k, torch.int32, (B,), dev, where, "seqused_k")
+    out, lse = _outputs(q, out, lse, (B, Hq), return_lse, dev, where)
+    if B == 0:
+        return out, lse
+    with _on(dev) as on:
+        workspace = _space(workspace, attn_decode_q4_workspace_size(B, Hq, Hkv, D), dev, where)
+        st = lib().attn_decode_paged_q4(_at(q), _at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta), _at(block_table),
+                                        block_table.shape[1], n, bs, _at(seqused_k), B, Hq, Hkv, D, gs, _scale(scale),
+                                        int(window_left), float(softcap), _at(out), _at(lse), _at(workspace),
+                                        workspace.numel(), on.stream(stream))
+    _check(st, where)
+    return out, lse
+
+
+def attn_fwd_varlen_paged_q4(q, k_cache, v_cache, k_meta, v_meta, *, block_table, cu_seqlens_q, max_seqlen_q,
+                             seqused_k, total_k, mask=MASK_NONE, scale=None, window_left=-1, softcap=0.0,
+                             out=None, lse=None, workspace=None, return_lse=True, stream=None):
+    """attn_fwd_varlen_paged over a 4-bit cache: packed q [total_q, Hq, D] bf16, the newest of
+    each sequence's seqused_k tokens -> (o [total_q, Hq, D] bf16, lse [Hq, total_q] fp32).
+
+    total_k: at least the sum of seqused_k (rows of the workspace); mask NONE or CAUSAL.
+    """
+    where = "attn_fwd_varlen_paged_q4"
+    dev = _cuda(q, where, "q")
+    total_q, Hq, D = q.shape
+    _tensor(seqused_k, torch.int32, (None,), dev, where, "seqused_k")
+    B = seqused_k.shape[0]
+    _tensor(cu_seqlens_q, torch.int32, (B + 1,), dev, where, "cu_seqlens_q")
+    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
+    _need(Dc == D, where, "q and the cache have different head_dims")
+    out, lse = _outputs(q, out, lse, (Hq, total_q), return_lse, dev, where)
+    if total_q == 0:
+        return out, lse
+    with _on(dev) as on:
+        workspace = _space(workspace, attn_fwd_q4_workspace_size(B, int(max_seqlen_q), Hq, Hkv, D, int(total_k)), dev, where)
+        st = lib().attn_fwd_varlen_paged_q4(_at(q), _at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta),
+                                            _at(block_table), block_table.shape[1], n, bs, _at(cu_seqlens_q),
+                                            _at(seqused_k), B, total_q, int(total_k), int(max_seqlen_q), Hq, Hkv, D, gs,
+                                            _scale(scale), int(mask), int(window_left), float(softcap), _at(out),
+                                            _at(lse), _at(workspace), workspace.numel(), on.stream(stream))
+    _check(st, where)
+    return out, lse

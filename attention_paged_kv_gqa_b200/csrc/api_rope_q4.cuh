@@ -1,0 +1,509 @@
+// api_rope_q4.cuh -- the C entry points of the rotary positions, the rotating KV
+// appends and the 4-bit cache (included by attn_api.cu, whose helpers it uses).
+#pragma once
+
+#include "q4.cuh"
+
+namespace {
+
+bool stride8(const int64_t* s, int n) {
+    for (int i = 0; i < n; ++i)
+        if (s[i] % 8) return false;
+    return true;
+}
+
+// Arguments of the table: cos_sin null means no rotation (where `optional`).
+attn_status_t check_rope(const float* cos_sin, int max_position, int rot_dim, const int32_t* positions, int n_axes,
+                         const int32_t* pair_axis, int D, bool optional) {
+    if (!cos_sin) return optional ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+    if (max_position <= 0 || rot_dim <= 0 || rot_dim > D || n_axes < 1) return ATTN_ERR_INVALID_ARG;
+    if (rot_dim % 16 || n_axes > kRopeMaxAxes) return ATTN_ERR_UNSUPPORTED;
+    if (!positions && !optional) return ATTN_ERR_INVALID_ARG;
+    if (n_axes > 1 && (!positions || !pair_axis)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(cos_sin)) return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+RopeTable rope_table(const float* cos_sin, int max_position, int rot_dim, const int32_t* positions, int n_axes,
+                     const int32_t* pair_axis, int interleaved, int inverse) {
+    RopeTable r;
+    r.table = cos_sin;
+    r.max_pos = max_position;
+    r.rot = cos_sin ? rot_dim : 0;
+    r.positions = positions;
+    r.axes = n_axes;
+    r.pair_axis = n_axes > 1 ? pair_axis : nullptr;
+    r.interleaved = interleaved ? 1 : 0;
+    r.sign = inverse ? -1.0f : 1.0f;
+    return r;
+}
+
+HeadRows head_rows(const void* p, const int64_t* strides) {
+    HeadRows h;
+    h.p = static_cast<const __nv_bfloat16*>(p);
+    h.row = p ? strides[0] : 0;
+    h.head = p ? strides[1] : 0;
+    return h;
+}
+
+// Warps that share a token's heads: one, unless that leaves the GPU without
+// enough loads in flight.
+int rope_parts(long long tokens, int passes, int sms) {
+    const long long want = (long long)sms * 16;
+    long long parts = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+    return (int)std::max<long long>(1, std::min<long long>(parts, passes));
+}
+
+// Heads of a block (the largest divisor of Hkv up to kQ4MaxHeads) and warps of a head.
+void q4_split(int Hkv, int NT, int* HB, int* SUB) {
+    int hb = std::min(Hkv, kQ4MaxHeads);
+    while (Hkv % hb) --hb;
+    *HB = hb;
+    *SUB = (NT == 1 ? 16 : 8) / hb;
+}
+
+size_t q4_workspace(int B, int Hkv, int D, int NT, int slots_of_grid) {
+    int HB, SUB;
+    q4_split(Hkv, NT, &HB, &SUB);
+    const size_t slots = (size_t)slots_of_grid + (size_t)(Hkv / HB) * B;
+    return slots * HB * 8 * NT * (D + 1) * sizeof(float) + (size_t)(B + 2) * sizeof(int);
+}
+
+bool q4_group_ok(int group_size, int D) {
+    return (group_size == 32 || group_size == 64 || group_size == 128) && group_size <= D;
+}
+
+template <int D, int GS, int NT>
+attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+    static std::atomic<uint64_t> attr_mask{0};   // one bit per device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_mask.load() & bit)) {
+        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, NT>, 227 * 1024);
+        if (s != ATTN_OK) return s;
+        attr_mask.fetch_or(bit);
+    }
+    q4_split(a.Hkv, NT, &a.HB, &a.SUB);
+    a.nhb = a.Hkv / a.HB;
+    const long long bound = (long long)a.B * a.max_blocks * a.nhb;
+    const int grid = (int)std::min<long long>(sms, bound);
+    const size_t slots = (size_t)grid + (size_t)a.nhb * a.B;
+    const size_t rows = slots * a.HB * 8 * NT;
+    if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < rows * (D + 1) * sizeof(float) + (size_t)(a.B + 2) * sizeof(int))
+        return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    a.o_part = static_cast<float*>(workspace);
+    a.lse_part = a.o_part + rows * D;
+    a.meta = reinterpret_cast<int*>(a.lse_part + rows);
+    using C = Q4Cfg<D, GS>;
+    int ns = 0;
+    while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= 227 * 1024) ++ns;
+    if (ns < 2) return ATTN_ERR_UNSUPPORTED;
+    a.nstages = ns;
+    q4_attn_kernel<D, GS, NT><<<grid, 32 * (a.HB * a.SUB + 1), C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st>>>(a);
+    attn_status_t s = launch_status();
+    if (s != ATTN_OK) return s;
+    const long long rows_out = (long long)a.B * a.max_q * a.Hq;
+    return launch_maybe_pdl(q4_combine_kernel<D, NT>, dim3((unsigned)((rows_out + 7) / 8)), dim3(256), 0, st, true, a);
+}
+
+template <int D, int GS>
+attn_status_t launch_q4_rows(const Q4AttnArgs& a, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
+    return a.max_q * a.group > 8 ? launch_q4_attn<D, GS, 2>(a, sms, ws, ws_bytes, st)
+                                 : launch_q4_attn<D, GS, 1>(a, sms, ws, ws_bytes, st);
+}
+
+attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
+    if (D == 128)
+        return GS == 128  ? launch_q4_rows<128, 128>(a, sms, ws, ws_bytes, st)
+               : GS == 64 ? launch_q4_rows<128, 64>(a, sms, ws, ws_bytes, st)
+                          : launch_q4_rows<128, 32>(a, sms, ws, ws_bytes, st);
+    return GS == 64 ? launch_q4_rows<64, 64>(a, sms, ws, ws_bytes, st) : launch_q4_rows<64, 32>(a, sms, ws, ws_bytes, st);
+}
+
+template <int D, int GS>
+attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
+    // a page and head per warp; every block builds the tables, so no more blocks than fill the GPU
+    const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv;
+    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 8));
+    q4_gather_kernel<D, GS><<<grid, 256, 2 * (a.B + 1) * sizeof(int), st>>>(a);
+    return launch_status();
+}
+
+attn_status_t launch_q4_gather(const Q4GatherArgs& a, int D, int GS, int sms, cudaStream_t st) {
+    if (D == 128)
+        return GS == 128  ? launch_q4_gather_t<128, 128>(a, sms, st)
+               : GS == 64 ? launch_q4_gather_t<128, 64>(a, sms, st)
+                          : launch_q4_gather_t<128, 32>(a, sms, st);
+    return GS == 64 ? launch_q4_gather_t<64, 64>(a, sms, st) : launch_q4_gather_t<64, 32>(a, sms, st);
+}
+
+// Checks of a 4-bit cache that every entry point shares.
+attn_status_t check_q4_cache(const void* k_cache, const void* v_cache, const void* k_meta, const void* v_meta,
+                             const int32_t* block_table, int max_blocks, int num_blocks, int block_size, int B, int Hkv,
+                             int D, int group_size) {
+    if (!k_cache || !v_cache || !k_meta || !v_meta || !block_table) return ATTN_ERR_INVALID_ARG;
+    if (B < 0 || Hkv <= 0 || max_blocks <= 0 || num_blocks <= 0) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (block_size != kPageRows || !q4_group_ok(group_size, D)) return ATTN_ERR_UNSUPPORTED;
+    if (B > kDecMaxSeqs) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)num_blocks * block_size >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)max_blocks * block_size >= (1LL << 30)) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)B * max_blocks >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;   // the page prefix is 32 bits
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_meta) || !aligned16(v_meta))
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+attn_status_t check_append(const void* q, const void* q_out, const void* k_new, const void* v_new, const int64_t* sq,
+                           const int64_t* sk, const int64_t* sv, const int32_t* cu_new, const int32_t* seqused_k,
+                           const int32_t* seqused_k_out, int B, int total_new, int Hq, int Hkv) {
+    if (!k_new || !v_new || !sk || !sv || !seqused_k) return ATTN_ERR_INVALID_ARG;
+    if ((q != nullptr) != (q_out != nullptr) || (q && !sq)) return ATTN_ERR_INVALID_ARG;
+    if (B < 0 || total_new < 0 || Hkv <= 0 || (q ? Hq <= 0 : Hq != 0)) return ATTN_ERR_INVALID_ARG;
+    if (!cu_new && total_new != B) return ATTN_ERR_INVALID_ARG;
+    if (seqused_k_out && seqused_k_out == seqused_k) return ATTN_ERR_INVALID_ARG;
+    if ((q && (!aligned16(q) || !aligned16(q_out) || !stride8(sq, 2))) || !aligned16(k_new) || !aligned16(v_new) ||
+        !stride8(sk, 2) || !stride8(sv, 2))
+        return ATTN_ERR_INVALID_ARG;
+    return ATTN_OK;
+}
+
+// Blocks of a kernel whose warp takes 1 / parts of a token; at least enough threads
+// for the lengths.
+attn_status_t append_grid(const RopeAppendArgs& a, unsigned* grid) {
+    const long long warps = std::max<long long>((long long)a.total_new * a.parts, 1);
+    const long long g = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (g >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    *grid = (unsigned)g;
+    return ATTN_OK;
+}
+
+}  // namespace
+
+attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, const int64_t* strides_q,
+                        const int64_t* strides_q_out, const int64_t* strides_k, const int64_t* strides_k_out, int total,
+                        int Hq, int Hkv, int D, const float* cos_sin, int max_position, int rot_dim,
+                        const int32_t* positions, int n_axes, const int32_t* pair_axis, int interleaved, int inverse,
+                        attn_stream_t stream) {
+    if (!q || !q_out || !strides_q || !strides_q_out) return ATTN_ERR_INVALID_ARG;
+    if ((k != nullptr) != (k_out != nullptr) || (k && (!strides_k || !strides_k_out))) return ATTN_ERR_INVALID_ARG;
+    if (total < 0 || Hq <= 0 || (k ? Hkv <= 0 : Hkv != 0)) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    attn_status_t s = check_rope(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, D, false);
+    if (s != ATTN_OK) return s;
+    if (!aligned16(q) || !aligned16(q_out) || !stride8(strides_q, 2) || !stride8(strides_q_out, 2))
+        return ATTN_ERR_INVALID_ARG;
+    if (k && (!aligned16(k) || !aligned16(k_out) || !stride8(strides_k, 2) || !stride8(strides_k_out, 2)))
+        return ATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (total == 0) return ATTN_OK;
+    RopeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = head_rows(q, strides_q);
+    a.k = head_rows(k, strides_k);
+    a.q_out = static_cast<__nv_bfloat16*>(q_out);
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.qo_row = strides_q_out[0];
+    a.qo_head = strides_q_out[1];
+    a.ko_row = k ? strides_k_out[0] : 0;
+    a.ko_head = k ? strides_k_out[1] : 0;
+    a.total = total;
+    a.Hq = Hq;
+    a.Hkv = k ? Hkv : 0;
+    a.r = rope_table(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, interleaved, inverse);
+    const int heads_at_once = 512 / D;
+    a.parts = rope_parts(total, (a.Hq + a.Hkv + heads_at_once - 1) / heads_at_once, sm_count(dev));
+    const long long grid = ((long long)total * a.parts + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+    if (grid >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (D == 128) rope_kernel<128><<<(unsigned)grid, kRopeThreads, 0, st>>>(a);
+    else rope_kernel<64><<<(unsigned)grid, kRopeThreads, 0, st>>>(a);
+    return launch_status();
+}
+
+attn_status_t attn_kv_append_rope_paged(const void* q, void* q_out, const void* k_new, const void* v_new,
+                                        const int64_t* strides_q, const int64_t* strides_k, const int64_t* strides_v,
+                                        void* k_cache, void* v_cache, const int32_t* block_table, int max_blocks_per_seq,
+                                        int num_blocks, int block_size, const int32_t* cu_seqlens_new,
+                                        const int32_t* seqused_k, int32_t* seqused_k_out, int B, int total_new, int Hq,
+                                        int Hkv, int D, const float* cos_sin, int max_position, int rot_dim,
+                                        const int32_t* positions, int n_axes, const int32_t* pair_axis, int interleaved,
+                                        int dtype, const float* descale_q, const float* descale_k,
+                                        const float* descale_v, attn_stream_t stream) {
+    attn_status_t s = check_append(q, q_out, k_new, v_new, strides_q, strides_k, strides_v, cu_seqlens_new, seqused_k,
+                                   seqused_k_out, B, total_new, Hq, Hkv);
+    if (s != ATTN_OK) return s;
+    if (!k_cache || !v_cache || !block_table || max_blocks_per_seq <= 0 || num_blocks <= 0) return ATTN_ERR_INVALID_ARG;
+    if (!dtype_ok(dtype)) return ATTN_ERR_INVALID_ARG;
+    if (dtype == ATTN_FP8_E4M3 && (!descale_k || !descale_v || (q && !descale_q))) return ATTN_ERR_INVALID_ARG;
+    if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+    if (block_size != kPageRows) return ATTN_ERR_UNSUPPORTED;
+    if ((long long)num_blocks * block_size >= (1LL << 31) || (long long)max_blocks_per_seq * block_size >= (1LL << 30))
+        return ATTN_ERR_UNSUPPORTED;
+    if ((s = check_rope(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, D, true)) != ATTN_OK) return s;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return ATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (B == 0) return ATTN_OK;
+    RopeAppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = head_rows(q, strides_q);
+    a.k = head_rows(k_new, strides_k);
+    a.v = head_rows(v_new, strides_v);
+    a.q_out = q_out;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.descale_q = descale_q;
+    a.descale_k = descale_k;
+    a.descale_v = descale_v;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cu_new = cu_seqlens_new;
+    a.seqused_k = seqused_k;
+    a.seqused_k_out = seqused_k_out;
+    a.B = B;
+    a.total_new = total_new;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.r = rope_table(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, interleaved, 0);
+    const int heads_at_once = 512 / D;
+    a.parts = rope_parts(total_new, (Hq + 2 * Hkv + heads_at_once - 1) / heads_at_once, sm_count(dev));
+    unsigned grid;
+    if ((s = append_grid(a, &grid)) != ATTN_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == ATTN_BF16) {
+        if (D == 128) rope_append_kernel<128, kCacheBf16><<<grid, kRopeThreads, 0, st>>>(a);
+        else rope_append_kernel<64, kCacheBf16><<<grid, kRopeThreads, 0, st>>>(a);
+    } else {
+        if (D == 128) rope_append_kernel<128, kCacheE4m3><<<grid, kRopeThreads, 0, st>>>(a);
+        else rope_append_kernel<64, kCacheE4m3><<<grid, kRopeThreads, 0, st>>>(a);
+    }
+    return launch_status();
+}
+
+attn_status_t attn_kv_append_paged_q4(const void* q, void* q_out, const void* k_new, const void* v_new,
+                                      const int64_t* strides_q, const int64_t* strides_k, const int64_t* strides_v,
+                                      void* k_cache, void* v_cache, void* k_meta, void* v_meta,
+                                      const int32_t* block_table, int max_blocks_per_seq, int num_blocks,
+                                      int block_size, const int32_t* cu_seqlens_new, const int32_t* seqused_k,
+                                      int32_t* seqused_k_out, int B, int total_new, int Hq, int Hkv, int D,
+                                      int group_size, const float* cos_sin, int max_position, int rot_dim,
+                                      const int32_t* positions, int n_axes, const int32_t* pair_axis, int interleaved,
+                                      attn_stream_t stream) {
+    attn_status_t s = check_append(q, q_out, k_new, v_new, strides_q, strides_k, strides_v, cu_seqlens_new, seqused_k,
+                                   seqused_k_out, B, total_new, Hq, Hkv);
+    if (s != ATTN_OK) return s;
+    if ((s = check_q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, max_blocks_per_seq, num_blocks, block_size, B,
+                            Hkv, D, group_size)) != ATTN_OK)
+        return s;
+    if ((s = check_rope(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, D, true)) != ATTN_OK) return s;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (B == 0) return ATTN_OK;
+    RopeAppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = head_rows(q, strides_q);
+    a.k = head_rows(k_new, strides_k);
+    a.v = head_rows(v_new, strides_v);
+    a.q_out = q_out;
+    a.k_cache = static_cast<uint8_t*>(k_cache);
+    a.v_cache = static_cast<uint8_t*>(v_cache);
+    a.k_meta = static_cast<uint16_t*>(k_meta);
+    a.v_meta = static_cast<uint16_t*>(v_meta);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cu_new = cu_seqlens_new;
+    a.seqused_k = seqused_k;
+    a.seqused_k_out = seqused_k_out;
+    a.B = B;
+    a.total_new = total_new;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.r = rope_table(cos_sin, max_position, rot_dim, positions, n_axes, pair_axis, interleaved, 0);
+    const int hq = 512 / D, hv = 256 / D;      // heads at once: of q, of k or v
+    a.parts = rope_parts(total_new, (Hq + hq - 1) / hq + 2 * ((Hkv + hv - 1) / hv), sm_count(dev));
+    unsigned grid;
+    if ((s = append_grid(a, &grid)) != ATTN_OK) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (D == 128) {
+        if (group_size == 128) rope_append_q4_kernel<128, 128><<<grid, kRopeThreads, 0, st>>>(a);
+        else if (group_size == 64) rope_append_q4_kernel<128, 64><<<grid, kRopeThreads, 0, st>>>(a);
+        else rope_append_q4_kernel<128, 32><<<grid, kRopeThreads, 0, st>>>(a);
+    } else {
+        if (group_size == 64) rope_append_q4_kernel<64, 64><<<grid, kRopeThreads, 0, st>>>(a);
+        else rope_append_q4_kernel<64, 32><<<grid, kRopeThreads, 0, st>>>(a);
+    }
+    return launch_status();
+}
+
+attn_status_t attn_kv_gather_paged_q4(const void* k_cache, const void* v_cache, const void* k_meta, const void* v_meta,
+                                      const int32_t* block_table, int max_blocks_per_seq, int num_blocks,
+                                      int block_size, const int32_t* cu_seqlens, const int32_t* starts, int B, int total,
+                                      int Hkv, int D, int group_size, void* k_out, void* v_out, attn_stream_t stream) {
+    attn_status_t s = check_q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, max_blocks_per_seq, num_blocks,
+                                     block_size, B, Hkv, D, group_size);
+    if (s != ATTN_OK) return s;
+    if (!cu_seqlens || !k_out || !v_out || total < 0) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return ATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (B == 0 || total == 0) return ATTN_OK;
+    Q4GatherArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k_cache = static_cast<const uint8_t*>(k_cache);
+    a.v_cache = static_cast<const uint8_t*>(v_cache);
+    a.k_meta = static_cast<const uint16_t*>(k_meta);
+    a.v_meta = static_cast<const uint16_t*>(v_meta);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cu = cu_seqlens;
+    a.starts = starts;
+    a.B = B;
+    a.total = total;
+    a.Hkv = Hkv;
+    a.k_out = static_cast<__nv_bfloat16*>(k_out);
+    a.v_out = static_cast<__nv_bfloat16*>(v_out);
+    return launch_q4_gather(a, D, group_size, sm_count(dev), static_cast<cudaStream_t>(stream));
+}
+
+size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 16) return 0;
+    return q4_workspace(B, Hkv, D, Hq / Hkv > 8 ? 2 : 1, current_sm_count_or(1024)) + 16;
+}
+
+attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_meta,
+                                   const void* v_meta, const int32_t* block_table, int max_blocks_per_seq,
+                                   int num_blocks, int block_size, const int32_t* seqused_k, int B, int Hq, int Hkv,
+                                   int D, int group_size, float softmax_scale, int window_left, float softcap, void* o,
+                                   float* lse, void* workspace, size_t workspace_bytes, attn_stream_t stream) {
+    if (!q || !o || !seqused_k) return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, max_blocks_per_seq, num_blocks,
+                                     block_size, B, Hkv, D, group_size);
+    if (s != ATTN_OK) return s;
+    if ((s = check_score_mods(ATTN_MASK_CAUSAL, window_left, softcap)) != ATTN_OK) return s;
+    if (Hq <= 0 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
+    if (Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (B == 0) return ATTN_OK;
+    Q4AttnArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.group = Hq / Hkv;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.max_q = 1;
+    a.total_q = B;
+    a.k_cache = static_cast<const uint8_t*>(k_cache);
+    a.v_cache = static_cast<const uint8_t*>(v_cache);
+    a.k_meta = static_cast<const uint16_t*>(k_meta);
+    a.v_meta = static_cast<const uint16_t*>(v_meta);
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.seqused_k = seqused_k;
+    a.scale = resolve_scale(softmax_scale, D);
+    a.causal = 1;
+    a.window = window_left < 0 ? -1 : std::min(window_left, 1 << 30);
+    a.softcap = softcap;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    return launch_q4(a, D, group_size, sm_count(dev), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+// The page stream serves up to 16 query rows per KV head; above that the pages are
+// read back as packed bf16 rows (exact) and the tensor-core forward runs on those.
+static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= 16; }
+
+size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int D, int total_k) {
+    if (B <= 0 || max_seqlen_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || total_k < 0) return 0;
+    const int group = Hq / Hkv;
+    if (q4_fwd_streams(max_seqlen_q, group))
+        return q4_workspace(B, Hkv, D, max_seqlen_q * group > 8 ? 2 : 1, current_sm_count_or(1024)) + 16;
+    return 2 * (size_t)std::max(total_k, 1) * Hkv * D * 2 + (size_t)(B + 1) * sizeof(int) + 16;
+}
+
+attn_status_t attn_fwd_varlen_paged_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_meta,
+                                       const void* v_meta, const int32_t* block_table, int max_blocks_per_seq,
+                                       int num_blocks, int block_size, const int32_t* cu_seqlens_q,
+                                       const int32_t* seqused_k, int B, int total_q, int total_k, int max_seqlen_q,
+                                       int Hq, int Hkv, int D, int group_size, float softmax_scale, int mask,
+                                       int window_left, float softcap, void* o, float* lse, void* workspace,
+                                       size_t workspace_bytes, attn_stream_t stream) {
+    if (!q || !o || !seqused_k || !cu_seqlens_q) return ATTN_ERR_INVALID_ARG;
+    attn_status_t s = check_q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, max_blocks_per_seq, num_blocks,
+                                     block_size, B, Hkv, D, group_size);
+    if (s != ATTN_OK) return s;
+    if (mask < ATTN_MASK_NONE || mask > ATTN_MASK_PATCH) return ATTN_ERR_INVALID_ARG;
+    if ((s = check_score_mods(mask, window_left, softcap)) != ATTN_OK) return s;
+    if (mask == ATTN_MASK_PATCH) return ATTN_ERR_UNSUPPORTED;
+    if (Hq <= 0 || Hq % Hkv || total_q < 0 || total_k < 0 || max_seqlen_q < 0) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
+    int dev = 0;
+    if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
+    if (B == 0 || total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int group = Hq / Hkv;
+    if (q4_fwd_streams(max_seqlen_q, group)) {
+        Q4AttnArgs a;
+        std::memset(&a, 0, sizeof(a));
+        a.B = B;
+        a.Hq = Hq;
+        a.Hkv = Hkv;
+        a.group = group;
+        a.q = static_cast<const __nv_bfloat16*>(q);
+        a.cu_q = cu_seqlens_q;
+        a.max_q = max_seqlen_q;
+        a.total_q = total_q;
+        a.k_cache = static_cast<const uint8_t*>(k_cache);
+        a.v_cache = static_cast<const uint8_t*>(v_cache);
+        a.k_meta = static_cast<const uint16_t*>(k_meta);
+        a.v_meta = static_cast<const uint16_t*>(v_meta);
+        a.block_table = block_table;
+        a.max_blocks = max_blocks_per_seq;
+        a.num_blocks = num_blocks;
+        a.seqused_k = seqused_k;
+        a.scale = resolve_scale(softmax_scale, D);
+        a.causal = mask == ATTN_MASK_CAUSAL ? 1 : 0;
+        a.window = window_left < 0 ? -1 : std::min(window_left, 1 << 30);
+        a.softcap = softcap;
+        a.o = static_cast<__nv_bfloat16*>(o);
+        a.lse = lse;
+        return launch_q4(a, D, group_size, sm_count(dev), workspace, workspace_bytes, st);
+    }
+    if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
+    if (workspace_bytes < attn_fwd_q4_workspace_size(B, max_seqlen_q, Hq, Hkv, D, total_k))
+        return ATTN_ERR_WORKSPACE_TOO_SMALL;
+    const size_t rows = (size_t)std::max(total_k, 1) * Hkv * D;
+    __nv_bfloat16* kw = static_cast<__nv_bfloat16*>(workspace);
+    __nv_bfloat16* vw = kw + rows;
+    int* cu_k = reinterpret_cast<int*>(vw + rows);
+    Q4GatherArgs g;
+    std::memset(&g, 0, sizeof(g));
+    g.k_cache = static_cast<const uint8_t*>(k_cache);
+    g.v_cache = static_cast<const uint8_t*>(v_cache);
+    g.k_meta = static_cast<const uint16_t*>(k_meta);
+    g.v_meta = static_cast<const uint16_t*>(v_meta);
+    g.block_table = block_table;
+    g.max_blocks = max_blocks_per_seq;
+    g.num_blocks = num_blocks;
+    g.lens = seqused_k;
+    g.cu_out = cu_k;
+    g.B = B;
+    g.total = total_k;
+    g.Hkv = Hkv;
+    g.k_out = kw;
+    g.v_out = vw;
+    if ((s = launch_q4_gather(g, D, group_size, sm_count(dev), st)) != ATTN_OK) return s;
+    return fwd_varlen_paged_impl(q, kw, vw, nullptr, 0, 0, 0, cu_seqlens_q, cu_k, nullptr, B, total_q, total_k,
+                                 max_seqlen_q, Hq, Hkv, D, softmax_scale, mask, nullptr, window_left, softcap, ATTN_BF16,
+                                 nullptr, nullptr, nullptr, o, lse, stream, 0);
+}

@@ -1372,3 +1372,5 @@ attn_status_t attn_decode_paged_noalloc(const void* q, const void* k_cache, cons
 }
 
 }  // extern "C"
+
+#include "api_rope_q4.cuh"

@@ -107,13 +107,17 @@ const char *attn_status_string(attn_status_t status);
  * synchronises `stream` (a debugging aid, not for hot loops).
  *   - A kernel gave up on a bounded wait since the last read: returns
  *     ATTN_ERR_DEVICE_TIMEOUT, *code_out names the wait (101..303 forward,
- *     401..402 decode, 601..604 backward, 901 the test hook below).  While that
+ *     401..402 decode, 541..542 4-bit decode,
+ *     601..604 backward, 901 the test hook below).  While that
  *     word is set, the other kernels' waits give up early.
  *   - Otherwise, a kernel met an index outside its buffers: returns
  *     ATTN_ERR_DEVICE_RANGE, *code_out names it (111 forward and 411 decode: a
  *     block_table entry outside [0, num_blocks), page 0 read in its place;
  *     501/502 KV append: a position past the block table / a page outside the
- *     cache, that token not written).  Nothing else stops on these.
+ *     cache, that token not written; 521/522 rotary positions: a position
+ *     outside the table, whose nearest row is used / an axis outside the given
+ *     ones, axis 0 used; 531 4-bit cache: more rows than the caller's total, the
+ *     rest left out).  Nothing else stops on these.
  *   - Neither: ATTN_OK and *code_out = 0.
  */
 attn_status_t attn_device_error(int *code_out, attn_stream_t stream);
@@ -434,6 +438,152 @@ attn_status_t attn_decode_paged_noalloc(
     int max_blocks_per_seq, int num_blocks, int block_size, const int32_t *seqused_k,
     int B, int num_heads_q, int num_heads_kv, int head_dim, float softmax_scale, int dtype,
     void *o, float *lse, attn_stream_t stream);
+
+/*
+ * Rotary positions of q and k, for the rotary options of "[CUDA] PagedAttention:
+ * add SM<80 fp16 fallback via memory-efficient attention" (Testing: rotary on and
+ * off, interleaved, packed QKV), before attn_fwd_* and, with inverse != 0, after
+ * attn_bwd_varlen: the gradient of a rotation is the inverse rotation.
+ *   y1 = x1 c - x2 s,  y2 = x2 c + x1 s   (inverse: s -> -s)
+ * for the pairs (x1, x2) = columns (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved != 0, i < rot_dim / 2; columns from rot_dim on are copied.  c and s
+ * are cos_sin[p][i] and cos_sin[p][rot_dim / 2 + i] with p = positions[axis][t].
+ *   q [total, Hq, D], k [total, Hkv, D] (NULL with Hkv 0: q alone) bf16, element
+ *                  strides {token, head} given per tensor (multiples of 8: views
+ *                  of a packed QKV tensor are taken as they are).
+ *   q_out, k_out   as q and k; either the input itself (in place) or memory that
+ *                  no input shares.
+ *   cos_sin        fp32 [max_position, rot_dim], 16-byte aligned.
+ *   positions      int32 [n_axes, total].
+ *   pair_axis      int32 [rot_dim / 2]: the axis of each pair (time, height and
+ *                  width of image and video tokens); not read with n_axes 1.
+ * A position outside [0, max_position) is reported (code 521 of
+ * attn_device_error) and the nearest row used.  Every product and sum is rounded
+ * to fp32, the result to bf16.  Supported: head_dim in {64, 128}, rot_dim a
+ * multiple of 16, n_axes <= 4.
+ */
+attn_status_t attn_rope(
+    const void *q, void *q_out, const void *k, void *k_out, const int64_t *strides_q,
+    const int64_t *strides_q_out, const int64_t *strides_k, const int64_t *strides_k_out, int total,
+    int num_heads_q, int num_heads_kv, int head_dim, const float *cos_sin, int max_position,
+    int rot_dim, const int32_t *positions, int n_axes, const int32_t *pair_axis, int interleaved,
+    int inverse, attn_stream_t stream);
+
+/*
+ * attn_kv_append_paged with the rotation, and for an e4m3 cache the
+ * quantisation, on the way: q is rotated into q_out, the new keys are rotated
+ * into their pages, the new values go into theirs.  Equal, bit for bit, to
+ * attn_rope followed by (for e4m3: x * (1 / descale) in fp32, rounded to nearest
+ * even, saturated at +-448, and) attn_kv_append_paged.
+ *   q            [total_new, Hq, D] bf16 (NULL with Hq 0 and q_out NULL: keys and
+ *                values alone); k_new, v_new [total_new, Hkv, D] bf16; element
+ *                strides {token, head} given per tensor, multiples of 8.
+ *   q_out        [total_new, Hq, D] contiguous, of the cache's type; not q itself.
+ *   k_cache, v_cache [num_blocks, block_size, Hkv, D] contiguous, of `dtype`.
+ *   cos_sin      as in attn_rope; NULL: no rotation (then max_position, rot_dim,
+ *                positions, n_axes and pair_axis are not read).
+ *   positions    int32 [n_axes, total_new]; NULL (n_axes 1): each token's position
+ *                in the cache.
+ *   descale_*    e4m3: device fp32 scalars, descale_q only with q.
+ *   others       as in attn_kv_append_paged.  Rows of q, k_new and v_new outside
+ *                [cu_seqlens_new[0], cu_seqlens_new[B]) are not read and theirs of
+ *                q_out not written.
+ * A token whose page or position is out of range is not written to the cache
+ * (codes 501, 502); its row of q_out is.  Supported: head_dim in {64, 128}.
+ */
+attn_status_t attn_kv_append_rope_paged(
+    const void *q, void *q_out, const void *k_new, const void *v_new, const int64_t *strides_q,
+    const int64_t *strides_k, const int64_t *strides_v, void *k_cache, void *v_cache,
+    const int32_t *block_table, int max_blocks_per_seq, int num_blocks, int block_size,
+    const int32_t *cu_seqlens_new, const int32_t *seqused_k, int32_t *seqused_k_out, int B,
+    int total_new, int num_heads_q, int num_heads_kv, int head_dim, const float *cos_sin,
+    int max_position, int rot_dim, const int32_t *positions, int n_axes, const int32_t *pair_axis,
+    int interleaved, int dtype, const float *descale_q, const float *descale_k,
+    const float *descale_v, attn_stream_t stream);
+
+/*
+ * The 4-bit KV cache.  Along head_dim every group_size (32, 64 or 128, at most
+ * head_dim) values x of a token and KV head share a step and a zero code.  With
+ * lo = min(x, 0) and hi = max(x, 0): step = (hi - lo) / 15 rounded up to 4
+ * significant bits (0 where that is below 2^-100, and then all codes are 0),
+ * zero = nearest(-lo / step); the code of x is nearest(x / step) + zero, ties to
+ * even, held within 0 .. 15, and stands for step * (code - zero): a bf16 number
+ * exactly, at most half a step from x.  A group that holds a NaN or an infinity,
+ * or whose hi - lo is past fp32, stands for NaN throughout.
+ *   k_cache, v_cache  bytes [num_blocks, Hkv, block_size * head_dim / 2]
+ *   k_meta, v_meta    16 bits [num_blocks, Hkv, block_size, head_dim / group_size]:
+ *                     step as bf16, whose lowest four bits are free and hold zero
+ * Nibble order (W = head_dim / 32; the low nibble of a byte first, words and
+ * 16-bit pieces little endian).  K: a token's row is head_dim / 2 bytes; dim
+ * 32 w + 8 c + e is nibble e of its 32-bit word c W + w.  V: a page's tile is one
+ * run; of token 8 a + 2 c + h, dim 32 u + 8 j + r is nibble j of the 16-bit piece
+ * (((8 a + r) 4 + c) W + u) 2 + h.
+ * The cache format is this library's own; no page describes one below 8 bits.
+ */
+
+/*
+ * Appends new tokens to a 4-bit cache: arguments as attn_kv_append_rope_paged,
+ * q_out bf16.  The keys are quantised from their rotated value in bf16, so the
+ * result is that of attn_rope followed by this call without a rotation.
+ */
+attn_status_t attn_kv_append_paged_q4(
+    const void *q, void *q_out, const void *k_new, const void *v_new, const int64_t *strides_q,
+    const int64_t *strides_k, const int64_t *strides_v, void *k_cache, void *v_cache, void *k_meta,
+    void *v_meta, const int32_t *block_table, int max_blocks_per_seq, int num_blocks,
+    int block_size, const int32_t *cu_seqlens_new, const int32_t *seqused_k,
+    int32_t *seqused_k_out, int B, int total_new, int num_heads_q, int num_heads_kv, int head_dim,
+    int group_size, const float *cos_sin, int max_position, int rot_dim, const int32_t *positions,
+    int n_axes, const int32_t *pair_axis, int interleaved, attn_stream_t stream);
+
+/*
+ * Reads tokens of a 4-bit cache back as packed bf16 rows (exactly): row
+ * cu_seqlens[b] + i of k_out and v_out [total, Hkv, D] receives token starts[b] + i
+ * (starts NULL: i) of sequence b, i < cu_seqlens[b + 1] - cu_seqlens[b].  Rows that
+ * no sequence owns, and tokens past a sequence's block table, are left as they
+ * are.  A page outside the cache is reported (code 411) and page 0 read.
+ */
+attn_status_t attn_kv_gather_paged_q4(
+    const void *k_cache, const void *v_cache, const void *k_meta, const void *v_meta,
+    const int32_t *block_table, int max_blocks_per_seq, int num_blocks, int block_size,
+    const int32_t *cu_seqlens, const int32_t *starts, int B, int total, int num_heads_kv,
+    int head_dim, int group_size, void *k_out, void *v_out, attn_stream_t stream);
+
+/*
+ * attn_decode_paged over a 4-bit cache: q [B, Hq, D] bf16, o [B, Hq, D] bf16,
+ * lse [B, Hq] fp32 or NULL; window_left, softcap and softmax_scale as there.
+ *   workspace    >= attn_decode_q4_workspace_size(...) bytes, 16-byte aligned; its
+ *                contents on entry do not matter.  Calls that could overlap on the
+ *                GPU need one each.
+ * Supported: head_dim in {64, 128}, Hq / Hkv <= 16, B <= 4096, any Hkv.
+ */
+size_t attn_decode_q4_workspace_size(int B, int num_heads_q, int num_heads_kv, int head_dim);
+attn_status_t attn_decode_paged_q4(
+    const void *q, const void *k_cache, const void *v_cache, const void *k_meta,
+    const void *v_meta, const int32_t *block_table, int max_blocks_per_seq, int num_blocks,
+    int block_size, const int32_t *seqused_k, int B, int num_heads_q, int num_heads_kv,
+    int head_dim, int group_size, float softmax_scale, int window_left, float softcap, void *o,
+    float *lse, void *workspace, size_t workspace_bytes, attn_stream_t stream);
+
+/*
+ * attn_fwd_varlen_paged over a 4-bit cache: packed queries [total_q, Hq, D] bf16,
+ * sequence b's the rows cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1 (at most
+ * max_seqlen_q) and the newest of its seqused_k[b] cached tokens; mask NONE or
+ * CAUSAL, window_left and softcap as there; lse [Hq, total_q] fp32 or NULL.
+ *   total_k      at least the sum of seqused_k: rows of the workspace (if it is less,
+ *                code 531 is reported and the last tokens are left out).
+ *   workspace    >= attn_fwd_q4_workspace_size(...) bytes, 16-byte aligned; as above.
+ * Up to 16 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
+ * pages as they are; more, to bf16 rows that the call reads back first.
+ */
+size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int num_heads_q, int num_heads_kv,
+                                  int head_dim, int total_k);
+attn_status_t attn_fwd_varlen_paged_q4(
+    const void *q, const void *k_cache, const void *v_cache, const void *k_meta,
+    const void *v_meta, const int32_t *block_table, int max_blocks_per_seq, int num_blocks,
+    int block_size, const int32_t *cu_seqlens_q, const int32_t *seqused_k, int B, int total_q,
+    int total_k, int max_seqlen_q, int num_heads_q, int num_heads_kv, int head_dim, int group_size,
+    float softmax_scale, int mask, int window_left, float softcap, void *o, float *lse,
+    void *workspace, size_t workspace_bytes, attn_stream_t stream);
 
 #ifdef __cplusplus
 }
