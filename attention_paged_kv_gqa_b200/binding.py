@@ -502,73 +502,88 @@ def attn_bwd_dense(q, k, v, o, dout, lse, *, causal=False, scale=None, window_le
 
 # ---------------------------------------------------------------- rotary positions, 4-bit cache
 # These calls check their tensors (type, shape, layout, device) before the pointers
-# leave for C, and run on the tensors' device whichever device is current.
+# leave for C, and run on the tensors' device whichever device is current.  A decode
+# step's kernels take a few microseconds, so the checks' passing path is kept short:
+# one comparison each, with the message worked out only for a tensor that fails.
+
+_BF16, _F32, _I32, _I16, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int16, torch.uint8
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
 
 def _need(ok, where, what):
     if not ok:
         raise ValueError("%s: %s" % (where, what))
 
 
-def _tensor(t, dtype, shape, dev, where, name, contiguous=True):
-    """t is a tensor of this type and shape (None: any extent) on this device."""
+def _refuse(t, dtype, shape, dev, where, name):
+    """Why t is not a contiguous tensor of this type and shape on this device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s: %s must be a tensor" % (where, name))
     if t.dtype != dtype:
         raise TypeError("%s: %s must be %s, got %s" % (where, name, dtype, t.dtype))
-    s = t.shape
-    if len(s) != len(shape) or any(b is not None and a != b for a, b in zip(s, shape)):
-        raise ValueError("%s: %s must have shape %s, got %s" % (where, name, tuple(shape), tuple(s)))
+    if t.shape != shape:
+        raise ValueError("%s: %s must have shape %s, got %s" % (where, name, tuple(shape), tuple(t.shape)))
     if t.device != dev:
         raise ValueError("%s: %s is on %s, not on %s" % (where, name, t.device, dev))
-    if contiguous and not t.is_contiguous():
-        raise ValueError("%s: %s must be contiguous" % (where, name))
+    raise ValueError("%s: %s must be contiguous" % (where, name))
 
 
-def _heads(t, H, D, total, dev, where, name):
-    """A bf16 [total, H, D] view with contiguous heads; returns its (token, head) strides."""
-    _tensor(t, torch.bfloat16, (total, H, D), dev, where, name, contiguous=False)
-    st = t.stride()
-    if st[2] != 1 or st[0] % 8 or st[1] % 8 or t.data_ptr() % 16:
+def _tensor(t, dtype, shape, dev, where, name):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _refuse(t, dtype, shape, dev, where, name)
+
+
+def _dims(t, n, where, name):
+    """The shape of a tensor of n dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: %s must be a tensor" % (where, name))
+    s = t.shape
+    if len(s) != n:
+        raise ValueError("%s: %s must have %s dimensions, got shape %s" %
+                         (where, name, ("no", "one", "two", "three", "four")[n], tuple(s)))
+    return s
+
+
+def _cuda(t, where, name):
+    """The shape and device of the [rows, heads, head_dim] tensor that leads a call."""
+    s = _dims(t, 3, where, name)
+    if not t.is_cuda:
+        raise ValueError("%s: %s must be a CUDA tensor" % (where, name))
+    return s, t.device
+
+
+_Strides = ctypes.c_int64 * 2
+
+
+def _heads(t, shape, dev, where, name):
+    """The (token, head) strides of a bf16 view with contiguous heads."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not _BF16 or t.shape != shape or t.device != dev:
+        _refuse(t, _BF16, shape, dev, where, name)
+    row, head, one = t.stride()
+    if one != 1 or (row | head) & 7 or t.data_ptr() & 15:
         raise ValueError("%s: %s needs a contiguous head_dim, strides that are multiples of 8 and a "
                          "16-byte aligned start" % (where, name))
-    return (ctypes.c_int64 * 2)(st[0], st[1])
+    return _Strides(row, head)
 
 
-class _on:
-    """Makes `dev` current for a call, and gives its stream."""
-
-    __slots__ = ("dev", "guard")
-
-    def __init__(self, dev):
-        self.dev = dev
-        self.guard = None
-
-    def __enter__(self):
-        if self.dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def stream(self, stream):
-        return (torch.cuda.current_stream(self.dev) if stream is None else stream).cuda_stream
+def _call(fn, dev, stream, *args):
+    """fn(*args, stream) with dev current (stream None: its current stream)."""
+    i = dev.index
+    if stream is not None:
+        raw = stream.cuda_stream
+    elif _raw_stream is not None:
+        raw = _raw_stream(i)
+    else:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() != i:
+        with torch.cuda.device(dev):
+            return fn(*args, raw)
+    return fn(*args, raw)
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
-
-
-def _cuda(t, where, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s: %s must be a tensor" % (where, name))
-    if t.dim() != 3:
-        raise ValueError("%s: %s must have three dimensions" % (where, name))
-    if t.device.type != "cuda":
-        raise ValueError("%s: %s must be a CUDA tensor" % (where, name))
-    return t.device
 
 
 def _rope_args(cos_sin, positions, pair_axis, total, dev, where, optional):
@@ -577,20 +592,21 @@ def _rope_args(cos_sin, positions, pair_axis, total, dev, where, optional):
         _need(optional, where, "cos_sin is required")
         _need(positions is None and pair_axis is None, where, "positions and pair_axis need cos_sin")
         return None, 0, 0, None, 1, None
-    _tensor(cos_sin, torch.float32, (None, None), dev, where, "cos_sin")
-    rows, rot = cos_sin.shape
+    rows, rot = _dims(cos_sin, 2, where, "cos_sin")
+    _tensor(cos_sin, _F32, (rows, rot), dev, where, "cos_sin")
     axes = 1
     if positions is None:
         _need(optional, where, "positions is required")
-    elif positions.dim() == 1:
-        _tensor(positions, torch.int32, (total,), dev, where, "positions")
+    elif isinstance(positions, torch.Tensor) and positions.dim() == 1:
+        _tensor(positions, _I32, (total,), dev, where, "positions")
     else:
-        _tensor(positions, torch.int32, (None, total), dev, where, "positions")
-        axes = positions.shape[0]
+        axes = _dims(positions, 2, where, "positions")[0]
+        _tensor(positions, _I32, (axes, total), dev, where, "positions")
     if pair_axis is not None:
-        _tensor(pair_axis, torch.int32, (rot // 2,), dev, where, "pair_axis")
-    _need(axes == 1 or pair_axis is not None, where, "several axes need pair_axis")
-    return _at(cos_sin), rows, rot, _at(positions), axes, _at(pair_axis)
+        _tensor(pair_axis, _I32, (rot // 2,), dev, where, "pair_axis")
+    elif axes != 1:
+        _need(False, where, "several axes need pair_axis")
+    return cos_sin.data_ptr(), rows, rot, _at(positions), axes, _at(pair_axis)
 
 
 def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=False, inverse=False,
@@ -604,59 +620,57 @@ def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=Fals
     way: the gradient of the forward rotation.  out_q / out_k may be q / k themselves.
     """
     where = "attn_rope"
-    dev = _cuda(q, where, "q")
-    total, Hq, D = q.shape
-    sq = _heads(q, Hq, D, total, dev, where, "q")
+    (total, Hq, D), dev = _cuda(q, where, "q")
+    sq = _heads(q, (total, Hq, D), dev, where, "q")
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, False)
     if out_q is None:
-        out_q = torch.empty((total, Hq, D), dtype=torch.bfloat16, device=dev)
-    so = _heads(out_q, Hq, D, total, dev, where, "out_q")
+        out_q = q.new_empty((total, Hq, D))
+    so = _heads(out_q, (total, Hq, D), dev, where, "out_q")
     Hkv, sk, sko = 0, None, None
     if k is not None:
-        _cuda(k, where, "k")
-        Hkv = k.shape[1]
-        sk = _heads(k, Hkv, D, total, dev, where, "k")
+        Hkv = _dims(k, 3, where, "k")[1]
+        sk = _heads(k, (total, Hkv, D), dev, where, "k")
         if out_k is None:
-            out_k = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
-        sko = _heads(out_k, Hkv, D, total, dev, where, "out_k")
+            out_k = k.new_empty((total, Hkv, D))
+        sko = _heads(out_k, (total, Hkv, D), dev, where, "out_k")
     else:
         _need(out_k is None, where, "out_k without k")
     if total == 0:
         return out_q, out_k
-    with _on(dev) as on:
-        st = lib().attn_rope(_at(q), _at(out_q), _at(k), _at(out_k), sq, so, sk, sko, total, Hq, Hkv, D, *rope,
-                             int(bool(interleaved)), int(bool(inverse)), on.stream(stream))
+    st = _call(lib().attn_rope, dev, stream, q.data_ptr(), out_q.data_ptr(), _at(k), _at(out_k), sq, so, sk, sko, total,
+               Hq, Hkv, D, *rope, 1 if interleaved else 0, 1 if inverse else 0)
     _check(st, where)
     return out_q, out_k
 
 
 def _append_args(q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, q_dtype, where):
-    dev = _cuda(k_new, where, "k_new")
-    total, Hkv, D = k_new.shape
-    sk = _heads(k_new, Hkv, D, total, dev, where, "k_new")
-    sv = _heads(v_new, Hkv, D, total, dev, where, "v_new")
+    (total, Hkv, D), dev = _cuda(k_new, where, "k_new")
+    sk = _heads(k_new, (total, Hkv, D), dev, where, "k_new")
+    sv = _heads(v_new, (total, Hkv, D), dev, where, "v_new")
     Hq, sq = 0, None
     if q is not None:
-        _cuda(q, where, "q")
-        Hq = q.shape[1]
-        sq = _heads(q, Hq, D, total, dev, where, "q")
+        Hq = _dims(q, 3, where, "q")[1]
+        sq = _heads(q, (total, Hq, D), dev, where, "q")
         if out_q is None:
-            out_q = torch.empty((total, Hq, D), dtype=q_dtype, device=dev)
-        _tensor(out_q, q_dtype, (total, Hq, D), dev, where, "out_q")
-        _need(out_q.data_ptr() % 16 == 0, where, "out_q must be 16-byte aligned")
+            out_q = q.new_empty((total, Hq, D), dtype=q_dtype)
+        else:
+            _tensor(out_q, q_dtype, (total, Hq, D), dev, where, "out_q")
+            _need(out_q.data_ptr() % 16 == 0, where, "out_q must be 16-byte aligned")
     else:
         _need(out_q is None, where, "out_q without q")
-    _tensor(seqused_k, torch.int32, (None,), dev, where, "seqused_k")
-    B = seqused_k.shape[0]
-    _tensor(block_table, torch.int32, (B, None), dev, where, "block_table")
+    B = _dims(seqused_k, 1, where, "seqused_k")[0]
+    _tensor(seqused_k, _I32, (B,), dev, where, "seqused_k")
+    mbps = _dims(block_table, 2, where, "block_table")[1]
+    _tensor(block_table, _I32, (B, mbps), dev, where, "block_table")
     if cu_seqlens_new is not None:
-        _tensor(cu_seqlens_new, torch.int32, (B + 1,), dev, where, "cu_seqlens_new")
+        _tensor(cu_seqlens_new, _I32, (B + 1,), dev, where, "cu_seqlens_new")
     else:
         _need(total == B, where, "without cu_seqlens_new there is one new token per sequence")
     if seqused_k_out is None:
         seqused_k_out = torch.empty_like(seqused_k)
-    _tensor(seqused_k_out, torch.int32, (B,), dev, where, "seqused_k_out")
-    return dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, seqused_k_out
+    else:
+        _tensor(seqused_k_out, _I32, (B,), dev, where, "seqused_k_out")
+    return dev, total, Hq, Hkv, D, B, mbps, sq, sk, sv, out_q, seqused_k_out
 
 
 def _same_lengths(seqused_k, used, dev, stream):
@@ -676,43 +690,44 @@ def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, se
     q may be None (q_out is then None).  positions None: each token's position in the cache.
     """
     where = "attn_kv_append_rope_paged"
-    fp8 = isinstance(k_cache, torch.Tensor) and k_cache.dtype == torch.float8_e4m3fn
-    kind = torch.float8_e4m3fn if fp8 else torch.bfloat16
-    dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, used = _append_args(
+    n, bs, _, _ = _dims(k_cache, 4, where, "k_cache")
+    fp8 = k_cache.dtype is torch.float8_e4m3fn
+    kind = torch.float8_e4m3fn if fp8 else _BF16
+    dev, total, Hq, Hkv, D, B, mbps, sq, sk, sv, out_q, used = _append_args(
         q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, kind, where)
-    _tensor(k_cache, kind, (None, None, Hkv, D), dev, where, "k_cache")
-    _tensor(v_cache, kind, tuple(k_cache.shape), dev, where, "v_cache")
+    _tensor(k_cache, kind, (n, bs, Hkv, D), dev, where, "k_cache")
+    _tensor(v_cache, kind, (n, bs, Hkv, D), dev, where, "v_cache")
     if fp8:
-        for name, d in (("descale_q", descale_q), ("descale_k", descale_k), ("descale_v", descale_v)):
-            if name != "descale_q" or q is not None:
-                _need(isinstance(d, torch.Tensor) and d.numel() == 1, where, name + " must be a one-element tensor")
-                _tensor(d, torch.float32, tuple(d.shape), dev, where, name)
+        for name, d in (("descale_k", descale_k), ("descale_v", descale_v), ("descale_q", descale_q)):
+            if q is None and name == "descale_q":
+                descale_q = None
+                continue
+            _need(isinstance(d, torch.Tensor) and d.numel() == 1, where, name + " must be a one-element tensor")
+            _tensor(d, _F32, d.shape, dev, where, name)
+    else:
+        descale_q = descale_k = descale_v = None
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
     if total == 0:
         return out_q, _same_lengths(seqused_k, used, dev, stream)
-    with _on(dev) as on:
-        st = lib().attn_kv_append_rope_paged(
-            _at(q), _at(out_q), _at(k_new), _at(v_new), sq, sk, sv, _at(k_cache), _at(v_cache), _at(block_table),
-            block_table.shape[1], k_cache.shape[0], k_cache.shape[1], _at(cu_seqlens_new), _at(seqused_k), _at(used),
-            B, total, Hq, Hkv, D, *rope, int(bool(interleaved)), FP8_E4M3 if fp8 else BF16,
-            _at(descale_q) if fp8 else None, _at(descale_k) if fp8 else None, _at(descale_v) if fp8 else None,
-            on.stream(stream))
+    st = _call(lib().attn_kv_append_rope_paged, dev, stream, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
+               sv, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mbps, n, bs, _at(cu_seqlens_new),
+               seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, *rope, 1 if interleaved else 0,
+               FP8_E4M3 if fp8 else BF16, _at(descale_q), _at(descale_k), _at(descale_v))
     _check(st, where)
     return out_q, used
 
 
-def _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where, Hkv=None, D=None):
+def _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where):
     """Checks a 4-bit cache -> (num_blocks, block_size, Hkv, D, group_size)."""
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("%s: k_cache must have shape [num_blocks, Hkv, block_size, head_dim / 2]" % where)
-    n, h, bs, half = k_cache.shape
-    _tensor(k_cache, torch.uint8, (n, h if Hkv is None else Hkv, bs, half if D is None else D // 2), dev, where, "k_cache")
-    _tensor(v_cache, torch.uint8, (n, h, bs, half), dev, where, "v_cache")
-    _tensor(k_meta, torch.int16, (n, h, bs, None), dev, where, "k_meta")
-    G = k_meta.shape[3]
-    _tensor(v_meta, torch.int16, (n, h, bs, G), dev, where, "v_meta")
-    _need(G > 0 and 2 * half % G == 0, where, "head_dim must be a multiple of the metas per token")
-    _tensor(block_table, torch.int32, (B, None), dev, where, "block_table")
+    s = _dims(k_cache, 4, where, "k_cache")
+    n, h, bs, half = s
+    _tensor(k_cache, _U8, s, dev, where, "k_cache")
+    _tensor(v_cache, _U8, s, dev, where, "v_cache")
+    G = _dims(k_meta, 4, where, "k_meta")[3]
+    _tensor(k_meta, _I16, (n, h, bs, G), dev, where, "k_meta")
+    _tensor(v_meta, _I16, (n, h, bs, G), dev, where, "v_meta")
+    if G < 1 or 2 * half % G:
+        _need(False, where, "head_dim must be a multiple of the metas per token")
     return n, bs, h, 2 * half, 2 * half // G
 
 
@@ -727,17 +742,18 @@ def attn_kv_append_paged_q4(q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, b
     in the header).
     """
     where = "attn_kv_append_paged_q4"
-    dev, total, Hq, Hkv, D, B, sq, sk, sv, out_q, used = _append_args(
-        q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, torch.bfloat16, where)
-    n, bs, _, _, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where, Hkv, D)
+    dev, total, Hq, Hkv, D, B, mbps, sq, sk, sv, out_q, used = _append_args(
+        q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, _BF16, where)
+    n, bs, h, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where)
+    if h != Hkv or Dc != D:
+        _need(False, where, "k_new and the cache have different heads")
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
     if total == 0:
         return out_q, _same_lengths(seqused_k, used, dev, stream)
-    with _on(dev) as on:
-        st = lib().attn_kv_append_paged_q4(
-            _at(q), _at(out_q), _at(k_new), _at(v_new), sq, sk, sv, _at(k_cache), _at(v_cache), _at(k_meta),
-            _at(v_meta), _at(block_table), block_table.shape[1], n, bs, _at(cu_seqlens_new), _at(seqused_k), _at(used),
-            B, total, Hq, Hkv, D, gs, *rope, int(bool(interleaved)), on.stream(stream))
+    st = _call(lib().attn_kv_append_paged_q4, dev, stream, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
+               sv, k_cache.data_ptr(), v_cache.data_ptr(), k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(),
+               mbps, n, bs, _at(cu_seqlens_new), seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, gs, *rope,
+               1 if interleaved else 0)
     _check(st, where)
     return out_q, used
 
@@ -749,56 +765,59 @@ def attn_kv_gather_paged_q4(k_cache, v_cache, k_meta, v_meta, block_table, cu_se
     Sequence b's tokens starts[b] .. (None: 0 ..) go to rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
     """
     where = "attn_kv_gather_paged_q4"
-    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.device.type != "cuda":
-        raise ValueError("%s: cu_seqlens must be a CUDA tensor" % where)
+    B = _dims(cu_seqlens, 1, where, "cu_seqlens")[0] - 1
+    _need(B >= 0 and cu_seqlens.is_cuda, where, "cu_seqlens must be a CUDA tensor of B + 1 entries")
     dev = cu_seqlens.device
-    _tensor(cu_seqlens, torch.int32, (None,), dev, where, "cu_seqlens")
-    B = cu_seqlens.shape[0] - 1
-    _need(B >= 0, where, "cu_seqlens must have B + 1 entries")
-    n, bs, Hkv, D, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
+    _tensor(cu_seqlens, _I32, (B + 1,), dev, where, "cu_seqlens")
+    n, bs, Hkv, D, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where)
+    mbps = _dims(block_table, 2, where, "block_table")[1]
+    _tensor(block_table, _I32, (B, mbps), dev, where, "block_table")
     if starts is not None:
-        _tensor(starts, torch.int32, (B,), dev, where, "starts")
+        _tensor(starts, _I32, (B,), dev, where, "starts")
+    total = int(total)
+    shape = (total, Hkv, D)
     if out_k is None:
-        out_k = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
+        out_k = torch.empty(shape, dtype=_BF16, device=dev)
+    else:
+        _tensor(out_k, _BF16, shape, dev, where, "out_k")
     if out_v is None:
-        out_v = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=dev)
-    _tensor(out_k, torch.bfloat16, (total, Hkv, D), dev, where, "out_k")
-    _tensor(out_v, torch.bfloat16, (total, Hkv, D), dev, where, "out_v")
+        out_v = torch.empty_like(out_k)
+    else:
+        _tensor(out_v, _BF16, shape, dev, where, "out_v")
     if total == 0:
         return out_k, out_v
-    with _on(dev) as on:
-        st = lib().attn_kv_gather_paged_q4(_at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta), _at(block_table),
-                                           block_table.shape[1], n, bs, _at(cu_seqlens), _at(starts), B, int(total),
-                                           Hkv, D, gs, _at(out_k), _at(out_v), on.stream(stream))
+    st = _call(lib().attn_kv_gather_paged_q4, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), k_meta.data_ptr(),
+               v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, cu_seqlens.data_ptr(), _at(starts), B, total, Hkv,
+               D, gs, out_k.data_ptr(), out_v.data_ptr())
     _check(st, where)
     return out_k, out_v
 
 
 def attn_decode_q4_workspace_size(B, num_heads_q, num_heads_kv, head_dim) -> int:
-    return int(lib().attn_decode_q4_workspace_size(B, num_heads_q, num_heads_kv, head_dim))
+    return lib().attn_decode_q4_workspace_size(B, num_heads_q, num_heads_kv, head_dim)
 
 
 def attn_fwd_q4_workspace_size(B, max_seqlen_q, num_heads_q, num_heads_kv, head_dim, total_k) -> int:
-    return int(lib().attn_fwd_q4_workspace_size(B, max_seqlen_q, num_heads_q, num_heads_kv, head_dim, total_k))
+    return lib().attn_fwd_q4_workspace_size(B, max_seqlen_q, num_heads_q, num_heads_kv, head_dim, total_k)
 
 
 def _outputs(q, out, lse, lse_shape, return_lse, dev, where):
-    _heads(q, q.shape[1], q.shape[2], q.shape[0], dev, where, "q")
-    _need(q.is_contiguous(), where, "q must be contiguous")
+    _tensor(q, _BF16, q.shape, dev, where, "q")
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-    _tensor(out, torch.bfloat16, tuple(q.shape), dev, where, "out")
-    if lse is None and return_lse:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=dev)
+        out = torch.empty_like(q)
+    else:
+        _tensor(out, _BF16, q.shape, dev, where, "out")
     if lse is not None:
-        _tensor(lse, torch.float32, lse_shape, dev, where, "lse")
+        _tensor(lse, _F32, lse_shape, dev, where, "lse")
+    elif return_lse:
+        lse = q.new_empty(lse_shape, dtype=_F32)
     return out, lse
 
 
-def _space(workspace, need, dev, where):
+def _space(workspace, need, q, dev, where):
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    _tensor(workspace, torch.uint8, (None,), dev, where, "workspace")
+        return q.new_empty((max(need, 16),), dtype=_U8)
+    _tensor(workspace, _U8, _dims(workspace, 1, where, "workspace"), dev, where, "workspace")
     return workspace
 
 
@@ -807,20 +826,22 @@ def attn_decode_paged_q4(q, k_cache, v_cache, k_meta, v_meta, block_table, sequs
                          return_lse=True, stream=None):
     """attn_decode_paged over a 4-bit cache: q [B, Hq, D] bf16 -> (o [B, Hq, D] bf16, lse [B, Hq] fp32)."""
     where = "attn_decode_paged_q4"
-    dev = _cuda(q, where, "q")
-    B, Hq, D = q.shape
-    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
-    _need(Dc == D, where, "q and the cache have different head_dims")
-    _tensor(seqused_k, torch.int32, (B,), dev, where, "seqused_k")
+    (B, Hq, D), dev = _cuda(q, where, "q")
+    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where)
+    if Dc != D:
+        _need(False, where, "q and the cache have different head_dims")
+    mbps = _dims(block_table, 2, where, "block_table")[1]
+    _tensor(block_table, _I32, (B, mbps), dev, where, "block_table")
+    _tensor(seqused_k, _I32, (B,), dev, where, "seqused_k")
     out, lse = _outputs(q, out, lse, (B, Hq), return_lse, dev, where)
     if B == 0:
         return out, lse
-    with _on(dev) as on:
-        workspace = _space(workspace, attn_decode_q4_workspace_size(B, Hq, Hkv, D), dev, where)
-        st = lib().attn_decode_paged_q4(_at(q), _at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta), _at(block_table),
-                                        block_table.shape[1], n, bs, _at(seqused_k), B, Hq, Hkv, D, gs, _scale(scale),
-                                        int(window_left), float(softcap), _at(out), _at(lse), _at(workspace),
-                                        workspace.numel(), on.stream(stream))
+    L = lib()
+    workspace = _space(workspace, L.attn_decode_q4_workspace_size(B, Hq, Hkv, D), q, dev, where)
+    st = _call(L.attn_decode_paged_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+               k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, seqused_k.data_ptr(), B, Hq, Hkv,
+               D, gs, _scale(scale), int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(),
+               workspace.numel())
     _check(st, where)
     return out, lse
 
@@ -834,22 +855,23 @@ def attn_fwd_varlen_paged_q4(q, k_cache, v_cache, k_meta, v_meta, *, block_table
     total_k: at least the sum of seqused_k (rows of the workspace); mask NONE or CAUSAL.
     """
     where = "attn_fwd_varlen_paged_q4"
-    dev = _cuda(q, where, "q")
-    total_q, Hq, D = q.shape
-    _tensor(seqused_k, torch.int32, (None,), dev, where, "seqused_k")
-    B = seqused_k.shape[0]
-    _tensor(cu_seqlens_q, torch.int32, (B + 1,), dev, where, "cu_seqlens_q")
-    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, block_table, B, dev, where)
-    _need(Dc == D, where, "q and the cache have different head_dims")
+    (total_q, Hq, D), dev = _cuda(q, where, "q")
+    B = _dims(seqused_k, 1, where, "seqused_k")[0]
+    _tensor(seqused_k, _I32, (B,), dev, where, "seqused_k")
+    _tensor(cu_seqlens_q, _I32, (B + 1,), dev, where, "cu_seqlens_q")
+    n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where)
+    if Dc != D:
+        _need(False, where, "q and the cache have different head_dims")
+    mbps = _dims(block_table, 2, where, "block_table")[1]
+    _tensor(block_table, _I32, (B, mbps), dev, where, "block_table")
     out, lse = _outputs(q, out, lse, (Hq, total_q), return_lse, dev, where)
     if total_q == 0:
         return out, lse
-    with _on(dev) as on:
-        workspace = _space(workspace, attn_fwd_q4_workspace_size(B, int(max_seqlen_q), Hq, Hkv, D, int(total_k)), dev, where)
-        st = lib().attn_fwd_varlen_paged_q4(_at(q), _at(k_cache), _at(v_cache), _at(k_meta), _at(v_meta),
-                                            _at(block_table), block_table.shape[1], n, bs, _at(cu_seqlens_q),
-                                            _at(seqused_k), B, total_q, int(total_k), int(max_seqlen_q), Hq, Hkv, D, gs,
-                                            _scale(scale), int(mask), int(window_left), float(softcap), _at(out),
-                                            _at(lse), _at(workspace), workspace.numel(), on.stream(stream))
+    L, most, total_k = lib(), int(max_seqlen_q), int(total_k)
+    workspace = _space(workspace, L.attn_fwd_q4_workspace_size(B, most, Hq, Hkv, D, total_k), q, dev, where)
+    st = _call(L.attn_fwd_varlen_paged_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+               k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, cu_seqlens_q.data_ptr(),
+               seqused_k.data_ptr(), B, total_q, total_k, most, Hq, Hkv, D, gs, _scale(scale), int(mask),
+               int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel())
     _check(st, where)
     return out, lse

@@ -54,19 +54,24 @@ int rope_parts(long long tokens, int passes, int sms) {
     return (int)std::max<long long>(1, std::min<long long>(parts, passes));
 }
 
-// Heads of a block (the largest divisor of Hkv up to kQ4MaxHeads) and warps of a head.
+constexpr int kQ4Smem = 227 * 1024 - 256;      // (some is static)
+
+// KV heads of a CTA's block, and warps of a head: the block with the most of the CTA's
+// warps at work, the largest such one (its copies are longest).
 void q4_split(int Hkv, int NT, int* HB, int* SUB) {
-    int hb = std::min(Hkv, kQ4MaxHeads);
-    while (Hkv % hb) --hb;
-    *HB = hb;
-    *SUB = (NT == 1 ? 16 : 8) / hb;
+    const int warps = q4_warps(NT);
+    int best = 1;
+    for (int hb = 2; hb <= std::min(Hkv, warps); ++hb)
+        if (Hkv % hb == 0 && hb * (warps / hb) >= best * (warps / best)) best = hb;
+    *HB = best;
+    *SUB = warps / best;
 }
 
-size_t q4_workspace(int B, int Hkv, int D, int NT, int slots_of_grid) {
+size_t q4_workspace(int B, int Hkv, int D, int NT, int sms) {
     int HB, SUB;
     q4_split(Hkv, NT, &HB, &SUB);
-    const size_t slots = (size_t)slots_of_grid + (size_t)(Hkv / HB) * B;
-    return slots * HB * 8 * NT * (D + 1) * sizeof(float) + (size_t)(B + 2) * sizeof(int);
+    const size_t slots = (size_t)sms + (size_t)(Hkv / HB) * B;
+    return slots * HB * 8 * NT * (D + 1) * sizeof(float);
 }
 
 bool q4_group_ok(int group_size, int D) {
@@ -80,32 +85,37 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_mask.load() & bit)) {
-        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, NT>, 227 * 1024);
+        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, NT>, kQ4Smem);
         if (s != ATTN_OK) return s;
         attr_mask.fetch_or(bit);
     }
     q4_split(a.Hkv, NT, &a.HB, &a.SUB);
     a.nhb = a.Hkv / a.HB;
-    const long long bound = (long long)a.B * a.max_blocks * a.nhb;
+    const long long bound = (long long)a.B * (a.max_blocks + kQ4Switch) * a.nhb;    // of the cost
+    if (bound >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     const int grid = (int)std::min<long long>(sms, bound);
     const size_t slots = (size_t)grid + (size_t)a.nhb * a.B;
     const size_t rows = slots * a.HB * 8 * NT;
     if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
-    if (workspace_bytes < rows * (D + 1) * sizeof(float) + (size_t)(a.B + 2) * sizeof(int))
+    if (workspace_bytes < rows * (D + 1) * sizeof(float))
         return ATTN_ERR_WORKSPACE_TOO_SMALL;
     a.o_part = static_cast<float*>(workspace);
     a.lse_part = a.o_part + rows * D;
-    a.meta = reinterpret_cast<int*>(a.lse_part + rows);
+    a.grid = grid;
     using C = Q4Cfg<D, GS>;
     int ns = 0;
-    while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= 227 * 1024) ++ns;
-    if (ns < 2) return ATTN_ERR_UNSUPPORTED;
+    while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= kQ4Smem) ++ns;
+    // a warp holds its pages and waits for the next ones: up to 4 SUB pages apart
+    if (ns < 3 * a.SUB + 1) return ATTN_ERR_UNSUPPORTED;
     a.nstages = ns;
-    q4_attn_kernel<D, GS, NT><<<grid, 32 * (a.HB * a.SUB + 1), C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st>>>(a);
+    const int spread = grid / std::max(1, a.nhb * a.B);
+    a.wpr = spread <= 8 ? 1 : spread <= 16 ? 2 : spread <= 32 ? 4 : 8;
+    q4_attn_kernel<D, GS, NT><<<grid, 32 * (q4_warps(NT) + 4), C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st>>>(a);
     attn_status_t s = launch_status();
     if (s != ATTN_OK) return s;
+    // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp
     const long long rows_out = (long long)a.B * a.max_q * a.Hq;
-    return launch_maybe_pdl(q4_combine_kernel<D, NT>, dim3((unsigned)((rows_out + 7) / 8)), dim3(256), 0, st, true, a);
+    return launch_maybe_pdl(q4_combine_kernel<D, NT>, dim3((unsigned)((rows_out * a.wpr + 7) / 8)), dim3(256), 0, st, true, a);
 }
 
 template <int D, int GS>

@@ -85,7 +85,9 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Group&
 }
 
 __device__ __forceinline__ float q4_step(uint32_t meta) { return __uint_as_float((meta << 16) & 0xfff00000u); }
-__device__ __forceinline__ float q4_zero(uint32_t meta) { return (float)(meta & 15u); }
+// (as a float whose significand ends in the integer: a conversion would go to the
+// quarter-rate unit that the exponentials need)
+__device__ __forceinline__ float q4_zero(uint32_t meta) { return __uint_as_float((meta & 15u) | 0x4b000000u) - 8388608.0f; }
 
 // ---------------------------------------------------------------- append
 // New tokens into 4-bit pages: q turned into q_out (bf16), k turned, rounded to
@@ -399,9 +401,13 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // sum is therefore taken out of the accumulators, which stay near their final size.
 // The running maximum moves only when a score exceeds it by 2^8, which a page
 // shows by one vote.
-constexpr int kQ4MaxHeads = 8;           // KV heads of a CTA's block
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
 constexpr int kQ4Recentre = 16;          // pages
+// Consumer warps of a CTA: as many as have the registers for 8 NT rows (and producer
+// warps for K, V, their metas and the queries).
+__host__ __device__ constexpr int q4_warps(int NT) { return NT == 1 ? 12 : 8; }
+constexpr int kQ4Switch = 4;             // pages that a change of sequence costs a CTA (for equal shares)
+constexpr float kQ4NoMax = -3.0e38f;     // the maximum before the first key (finite: differences with it stay numbers)
 
 struct Q4AttnArgs {
     int B, Hq, Hkv, group;
@@ -421,8 +427,9 @@ struct Q4AttnArgs {
     float softcap;           // 0: none
     float* o_part;           // [slots][HB][8 NT][D]
     float* lse_part;         // [slots][HB][8 NT]
-    int* meta;               // [B + 1] page prefix, then pages per CTA
+    int grid;                // CTAs
     int nstages;
+    int wpr;                 // combine: warps of a row (1, 2, 4 or 8)
     __nv_bfloat16* o;        // as q
     float* lse;              // [Hq][total_q], or [B][Hq] (cu_q null); or null
 };
@@ -433,12 +440,17 @@ struct Q4Cfg {
     static constexpr int META = kPageRows * (D / GS) * 2;       // bytes of its metas
     __host__ __device__ static constexpr int stage_bytes(int HB) { return 2 * HB * (TILE + META); }
     __host__ __device__ static constexpr int merge_bytes(int HB, int SUB, int NT) {
-        // per exchange slot: the accumulators of a warp, its maxima and sums
-        return SUB > 1 ? HB * ((SUB + 1) / 2) * 32 * (D / 16 * NT * 4 + NT * 4) * 4 : 0;
+        // per exchange slot: the accumulators of a warp, its maxima, sums and beta
+        return SUB > 1 ? HB * ((SUB + 1) / 2) * 32 * (D / 16 * NT * 4 + NT * 4 + 2) * 4 : 0;
     }
-    __host__ __device__ static constexpr int table_bytes(int B) { return ((2 * B + 2) * 4 + 15) / 16 * 16; }
+    // the queries of a segment, twice: the B fragments of Q^T, then per row the units and sums
+    static constexpr int QROWS = 1 + D / GS;
+    __host__ __device__ static constexpr int query_bytes(int HB, int NT) {
+        return HB * (NT * (D / 32) * 512 + QROWS * 8 * NT * 4);
+    }
+    __host__ __device__ static constexpr int table_bytes(int B) { return ((3 * B + 2) * 4 + 15) / 16 * 16; }
     __host__ __device__ static constexpr int smem_bytes(int HB, int SUB, int NT, int B, int ns) {
-        return 128 + ns * stage_bytes(HB) + merge_bytes(HB, SUB, NT) + table_bytes(B) + 2 * ns * 8;
+        return ns * stage_bytes(HB) + 2 * query_bytes(HB, NT) + merge_bytes(HB, SUB, NT) + table_bytes(B) + (2 * ns + 4) * 8;
     }
 };
 
@@ -451,41 +463,164 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
         : "memory");
 }
 
+// D += A B and D = A B (no accumulator to clear), not volatile: free to be scheduled.
+__device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void q4_mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void q4_mma2(float2 (&d)[2], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// N consecutive words (N = 2 or 4, aligned) of shared memory.
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
+    }
+}
+
+// The N metas (1, 2 or 4) of a token.
+template <int N>
+__device__ __forceinline__ void load_metas(const uint8_t* p, uint32_t (&m)[N]) {
+    if constexpr (N == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        m[0] = x.x & 0xffffu, m[1] = x.x >> 16, m[2] = x.y & 0xffffu, m[3] = x.y >> 16;
+    } else if constexpr (N == 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        m[0] = x & 0xffffu, m[1] = x >> 16;
+    } else {
+        m[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+}
+
 // Keys the sequence's queries can see start here (the window of its first query).
 __device__ __forceinline__ int q4_first_key(int L, int n, int window) {
     return window >= 0 ? max(0, L - n - window) : 0;
 }
 
+// Pages that sequence b's queries read, of one block of KV heads.
+__device__ __forceinline__ int q4_queries(const Q4AttnArgs& a, int b) {
+    return a.cu_q ? min(max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0), a.max_q) : 1;
+}
+__device__ __forceinline__ int q4_pages(const Q4AttnArgs& a, int b) {
+    const int L = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows), n = q4_queries(a, b);
+    return n > 0 ? (L + kPageRows - 1) / kPageRows - q4_first_key(L, n, a.window) / kPageRows : 0;
+}
+// The cost of a CTA's share, PC that of all pages of one block of heads: equal ones, of a
+// pair of pages per warp at least.
+__device__ __forceinline__ int q4_share(int PC, const Q4AttnArgs& a) {
+    return max((int)(((long long)PC * a.nhb + a.grid - 1) / a.grid), 2 * a.SUB);
+}
+
+// Eight query rows (row0 ..) of a KV head, for a sequence of n queries: their B fragments (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of
+// each word in f16 (second nibbles' dims over 16), and per row the unit of its raw scores in
+// log2 units and minus the sums of q over the groups.  Rows past the last query are zero.
 template <int D, int GS, int NT>
-__global__ void __launch_bounds__(NT == 1 ? 544 : 288, 1) q4_attn_kernel(const Q4AttnArgs a) {
+__device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int group, float unit, int n, int row0, uint32_t frag_at,
+                                        uint32_t rows_at) {
+    // (q: the first query of the sequence, at the KV head's first query head; offsets in shared memory)
+    extern __shared__ __align__(128) uint8_t q4_smem[];
+    uint4* frag = reinterpret_cast<uint4*>(q4_smem + frag_at);
+    float* rows = reinterpret_cast<float*>(q4_smem + rows_at);
+    const int lane = threadIdx.x & 31;
+    constexpr int W = D / 32, G = D / GS, WG = W / G;
+    const int r8 = lane >> 2, t4 = lane & 3, row = row0 + r8, tok = n == 1 ? row >= group : row / group;
+    const bool live = tok < n;
+    const __nv_bfloat16* qr = q + (live ? ((long long)tok * Hq + row - tok * group) * D : 0);
+    uint4 x[W];
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        x[w] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * w + 8 * t4)) : make_uint4(0, 0, 0, 0);
+    float big = 0.0f, sum[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sum[g] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const uint32_t xs[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            big = fmax3(big, fabsf(bf16_lo(xs[e])), fabsf(bf16_hi(xs[e])));
+            sum[w / WG] += bf16_lo(xs[e]) + bf16_hi(xs[e]);
+        }
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+    }
+    // the largest q of the row to [2^13, 2^14)
+    const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 115);
+    const float up = __uint_as_float((uint32_t)(127 + 13 - ex) << 23), up1 = up * 0.0625f;
+    const float down = __uint_as_float((uint32_t)(127 + 11 + ex) << 23);    // 2^24 / up
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+        frag[w * 32 + lane] = make_uint4(pack_f16(bf16_lo(x[w].x) * up, bf16_lo(x[w].z) * up),
+                                         pack_f16(bf16_hi(x[w].x) * up1, bf16_hi(x[w].z) * up1),
+                                         pack_f16(bf16_lo(x[w].y) * up, bf16_lo(x[w].w) * up),
+                                         pack_f16(bf16_hi(x[w].y) * up1, bf16_hi(x[w].w) * up1));
+    if (t4 == 0) {
+        rows[row] = down * unit;
+#pragma unroll
+        for (int g = 0; g < G; ++g) rows[(1 + g) * 8 * NT + row] = -sum[g] / down;
+    }
+}
+
+template <int D, int GS, int NT>
+__global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(const Q4AttnArgs a) {
     using C = Q4Cfg<D, GS>;
     constexpr int W = D / 32;            // words of a lane's K row piece; V words per token pair
     constexpr int G = D / GS;            // groups of a head
     constexpr int WG = W / G;            // words of a group
     constexpr int MT = D / 16;           // 16-column output tiles
+    constexpr int NP = NT == 1 ? 2 : 1;  // pages a warp takes at once: two chains of dependent operations side by side
     const int NS = a.nstages, HB = a.HB, SUB = a.SUB, SB = C::stage_bytes(HB);
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) & ~uintptr_t(127));
-    float* mrg = reinterpret_cast<float*>(smem + NS * SB);
-    int* prefix = reinterpret_cast<int*>(smem + NS * SB + C::merge_bytes(HB, SUB, NT));   // [B + 1]
-    int* lenv = prefix + (a.B + 1);                                                     // [B]
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + NS * SB + C::merge_bytes(HB, SUB, NT) + C::table_bytes(a.B));
+    extern __shared__ __align__(128) uint8_t q4_smem[];
+    uint8_t* smem = q4_smem;
+    uint8_t* tail = smem + NS * SB;
+    uint8_t* qarea = tail;                           // two of: [HB][NT][W][32] uint4, [HB][QROWS][8 NT] float
+    const int QB = C::query_bytes(HB, NT);
+    tail += 2 * QB;
+    float* mrg = reinterpret_cast<float*>(tail);
+    tail += C::merge_bytes(HB, SUB, NT);
+    int* prefix = reinterpret_cast<int*>(tail);      // [B + 1] pages before sequence b
+    int* cost = prefix + (a.B + 1);                  // [B + 1] their cost
+    int* lenv = cost + (a.B + 1);                    // [B]
+    uint64_t* full = reinterpret_cast<uint64_t*>(tail + C::table_bytes(a.B));
     uint64_t* empty = full + NS;
+    uint64_t *qfull = empty + NS, *qempty = qfull + 2;
+    __shared__ int bounds[2], first_place[2];        // the share's first page and the one behind it; its first sequence
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cap = a.max_blocks * kPageRows;
-    auto queries = [&](int b) { return a.cu_q ? min(max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0), a.max_q) : 1; };
+    // (by way of a shuffle: what depends on the warp alone then stays off the vector units)
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    auto queries = [&](int b) { return q4_queries(a, b); };
     if (warp == 0) {
-        int run = 0;
+        int run = 0, with_any = 0;
         for (int base = 0; base < a.B; base += 32) {
             const int b = base + lane;
             int cnt = 0;
             if (b < a.B) {
-                const int L = min(max(a.seqused_k[b], 0), cap), n = queries(b);
-                lenv[b] = L;
-                if (n > 0) cnt = (L + kPageRows - 1) / kPageRows - q4_first_key(L, n, a.window) / kPageRows;
+                lenv[b] = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows);
+                cnt = q4_pages(a, b);
             }
             int incl = cnt;
 #pragma unroll
@@ -493,257 +628,268 @@ __global__ void __launch_bounds__(NT == 1 ? 544 : 288, 1) q4_attn_kernel(const Q
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
-            if (b < a.B) prefix[b] = run + incl - cnt;
+            const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0);
+            if (b < a.B) {
+                prefix[b] = run + incl - cnt;
+                cost[b] = run + incl - cnt + kQ4Switch * (with_any + __popc(any & ((1u << lane) - 1u)));
+            }
             run += __shfl_sync(0xffffffffu, incl, 31);
+            with_any += __popc(any);
         }
-        if (lane == 0) prefix[a.B] = run;
+        if (lane == 0) {
+            prefix[a.B] = run;
+            cost[a.B] = run + kQ4Switch * with_any;
+        }
+        __syncwarp();
+        // The pages of one head block after another, each sequence's behind kQ4Switch units for
+        // the change to it, are cut into equal shares of this cost (their number stays below
+        // 2^31, as the host checks).  Where this CTA's share starts and ends:
+        const int PC = run + kQ4Switch * with_any, share = q4_share(PC, a);
+        for (int e = 0; e < 2; ++e) {
+            const long long c = (long long)(blockIdx.x + e) * share;
+            int hb = 0, at = run * a.nhb, b = 0;
+            if (c < (long long)PC * a.nhb) {
+                hb = a.nhb == 1 ? 0 : (int)c / PC;
+                const int r = (int)c - hb * PC;
+                // the largest b with cost[b] <= r, 32 candidates at a time
+                for (int len = a.B; len > 1;) {
+                    const int step = (len + 31) / 32, i = lane * step;
+                    const int k = __popc(__ballot_sync(0xffffffffu, i < len && cost[b + min(i, len - 1)] <= r)) - 1;
+                    b += k * step;
+                    len = min(step, len - k * step);
+                }
+                at = hb * run + prefix[b] + max(r - cost[b] - kQ4Switch, 0);
+            }
+            if (lane == 0) {
+                bounds[e] = at;
+                if (e == 0) {
+                    first_place[0] = hb;
+                    first_place[1] = b;
+                }
+            }
+        }
     }
     if (threadIdx.x == 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], 3);
             mbar_init(&empty[i], HB);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 1);
+            mbar_init(&qempty[i], HB * SUB);
         }
         fence_mbar_init();
     }
     __syncthreads();
-    const int P = prefix[a.B];                       // pages of one head block
-    const long long total = (long long)P * a.nhb;
-    const long long ppc = (total + gridDim.x - 1) / gridDim.x;
-    const long long p0 = min(total, blockIdx.x * ppc), p1 = min(total, p0 + ppc);
-    if (blockIdx.x == 0) {
-        for (int b = threadIdx.x; b <= a.B; b += blockDim.x) a.meta[b] = prefix[b];
-        if (threadIdx.x == 0) a.meta[a.B + 1] = (int)ppc;
-    }
-    auto seq_of = [&](int g) {                       // the largest b with prefix[b] <= g
-        int lo = 0, hi = a.B;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= g) lo = mid; else hi = mid;
-        }
-        return lo;
-    };
-    const int npages = (int)(p1 - p0);
+    const int P = prefix[a.B], p0 = bounds[0], npages = bounds[1] - p0;
+    if (npages == 0) return;
 
-    if (warp == HB * SUB) {
-        // ------------------------------------------------------------ producer
+    // The queries of the share's sequences as the consumers want them, in two areas by turns:
+    // the first sequence's by the consumers themselves, the others one sequence ahead by the
+    // fourth producer warp.
+    auto prepare = [&](int turn, int hb, int b, int first, int step) {
+        const uint32_t to = (uint32_t)(qarea - smem) + (turn & 1) * QB;
+        const __nv_bfloat16* q = a.q + ((long long)(a.cu_q ? __ldg(&a.cu_q[b]) : b) * a.Hq + hb * HB * a.group) * D;
+        const int n = queries(b);
+        for (int t = first; t < HB * NT; t += step)
+            q4_prepare<D, GS, NT>(q + t / NT * a.group * D, a.Hq, a.group, a.scale * kLog2e, n, t % NT * 8, to + t * W * 512,
+                                  to + HB * NT * W * 512 + t / NT * C::QROWS * 32 * NT);
+    };
+    // The sequences of the share in order: (block of heads, sequence), and the page at which each ends.
+    struct Place {
+        int hb, b, end;
+    };
+    auto ends = [&](int hb, int b) { return min(npages, hb * P + prefix[b + 1] - p0); };
+    auto next_place = [&](Place x) {                 // the next sequence that has pages
+        do {
+            if (++x.b == a.B) {
+                x.b = 0;
+                ++x.hb;
+            }
+        } while (prefix[x.b + 1] == prefix[x.b]);
+        x.end = ends(x.hb, x.b);
+        return x;
+    };
+    const Place start = {first_place[0], first_place[1], ends(first_place[0], first_place[1])};
+
+    if (warp >= q4_warps(NT)) {
+        // ------------------------------------------------------------ producers: K, V, metas, queries
+        const int which = warp - q4_warps(NT);
+        if (which == 3) {
+            Place x = start;
+            for (int turn = 1; x.end < npages; ++turn) {
+                x = next_place(x);
+                bool ok = mbar_wait(&qempty[turn & 1], (turn >> 1 & 1) ^ 1, kErrQ4Empty);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                prepare(turn, x.hb, x.b, 0, 1);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&qfull[turn & 1]);
+            }
+            return;
+        }
+        const uint8_t* src = which == 0 ? a.k_cache : which == 1 ? a.v_cache : reinterpret_cast<const uint8_t*>(a.k_meta);
+        const uint8_t* src2 = reinterpret_cast<const uint8_t*>(a.v_meta);
+        const int unit = which < 2 ? C::TILE : C::META, bytes = HB * unit;
+        uint8_t* dst0 = smem + which * HB * C::TILE;
         const uint64_t pol = policy_evict_first();
-        int issued = 0;
+        int issued = 0, st = 0;
+        uint32_t ph = 1;
+        Place x = start;
         for (int base = 0; base < npages; base += 32) {
-            int phys = 0, hb = 0;
+            long long mine = 0;                      // this lane's page of the next 32: its first tile
             if (base + lane < npages) {
-                const long long vg = p0 + base + lane;
-                hb = (int)(vg / P);
-                const int g = (int)(vg % P);
-                const int b = seq_of(g);
+                while (x.end <= base + lane) x = next_place(x);
+                const int hb = x.hb, b = x.b, g = p0 + base + lane - hb * P;
                 const int slot = g - prefix[b] + q4_first_key(lenv[b], queries(b), a.window) / kPageRows;
-                phys = a.block_table[(long long)b * a.max_blocks + slot];
+                int phys = a.block_table[(long long)b * a.max_blocks + slot];
                 if (phys < 0 || phys >= a.num_blocks) {
                     record_data_error(kErrDecPageRange);   // outside the cache: reported, page 0 read
                     phys = 0;
                 }
+                mine = ((long long)phys * a.Hkv + hb * HB) * unit;
             }
             const int cnt = min(32, npages - base);
             bool ok = true;
             for (int i = 0; i < cnt; ++i, ++issued) {
-                const long long tile = (long long)__shfl_sync(0xffffffffu, phys, i) * a.Hkv +
-                                       __shfl_sync(0xffffffffu, hb, i) * HB;
-                const int st = issued % NS;
-                ok = mbar_wait(&empty[st], ((issued / NS) & 1) ^ 1, kErrQ4Empty);
+                const long long at = __shfl_sync(0xffffffffu, mine, i);
+                ok = mbar_wait(&empty[st], ph, kErrQ4Empty);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                uint8_t* dst = smem + st * SB;
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], SB);
-                __syncwarp();
-                if (lane < 2)
-                    bulk_load(dst + lane * HB * C::TILE, (lane ? a.v_cache : a.k_cache) + tile * C::TILE, HB * C::TILE,
-                              &full[st], pol);
-                else if (lane < 4)
-                    bulk_load(dst + 2 * HB * C::TILE + (lane - 2) * HB * C::META,
-                              (lane == 3 ? a.v_meta : a.k_meta) + tile * (C::META / 2), HB * C::META, &full[st], pol);
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[st], which < 2 ? bytes : 2 * bytes);
+                    bulk_load(dst0 + st * SB, src + at, bytes, &full[st], pol);
+                    if (which == 2) bulk_load(dst0 + st * SB + bytes, src2 + at, bytes, &full[st], pol);
+                }
+                if (++st == NS) {
+                    st = 0;
+                    ph ^= 1;
+                }
             }
             if (!ok) break;
         }
         if (lane == 0) {
-            for (int st = 0; st < NS && st < issued; ++st) {
-                const int last = st + ((issued - 1 - st) / NS) * NS;
-                mbar_wait_drain(&full[st], (last / NS) & 1, kErrQ4Full);
+            for (int s = 0; s < NS && s < issued; ++s) {
+                const int last = s + ((issued - 1 - s) / NS) * NS;
+                mbar_wait_drain(&full[s], (last / NS) & 1, kErrQ4Full);
             }
         }
         return;
     }
-    if (warp > HB * SUB) return;
+    if (warp >= HB * SUB) return;
     // ---------------------------------------------------------------- consumers
     const int h = warp / SUB, sub = warp % SUB;      // head of the block, this warp's share of its pages
     const int r8 = lane >> 2, t4 = lane & 3;
     const bool capped = a.softcap > 0.0f;
-    uint32_t qb[NT][W][4];               // B fragments of Q^T: (dims e = 0, 4), (1, 5), (2, 6), (3, 7)
-    float qs[NT][2][G];                  // sum of q over a group, in units of the raw score
-    float kf[NT][2];                     // score in natural units = raw score * kf
-    float acc[MT][NT][4];                // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
-    float zac[NT][2][G];                 // sum w zero, this lane's keys
-    float m[NT][2], l[NT][2];            // maximum (log2 units) and sum (this lane's keys)
-    float beta = 1.0f, cap_step = 0.0f;  // w = p step beta; steps below cap_step are in range
+    // this lane's B fragments of Q^T, (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word: in
+    // shared memory, which spares registers
+    uint32_t qb = 0;                     // (its offset in shared memory)
+    // of the columns 2 t4 and 2 t4 + 1 (x, y) of each 8-row tile:
+    float2 qs[NT][G];                    // minus the sum of q over a group, in units of the raw score
+    float2 kf[NT];                       // score in log2 units = raw score * kf
+    float2 acc[MT][NT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
+    float2 zac[NT][G];                   // sum w zero, this lane's keys
+    float2 m[NT], l[NT];                 // minus the maximum (log2 units); sum, this lane's keys
+    float2 thr[NT];                      // the raw score that moves the maximum
+    float beta = 1.0f;                   // w = p step beta
+    uint32_t cap_meta = 0;               // metas below it have steps that beta keeps in range
     int since = 0;
-    auto load_q = [&](int b, int n, int hq0) {
-        const long long tok0 = a.cu_q ? __ldg(&a.cu_q[b]) : b;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = nt * 8 + r8;
-            const int tok = row / a.group;
-            const bool live = tok < n;
-            const __nv_bfloat16* qr = a.q + ((tok0 + (live ? tok : 0)) * a.Hq + hq0 + (live ? row % a.group : 0)) * D;
-            uint4 x[W];
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-                x[w] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * w + 8 * t4)) : make_uint4(0, 0, 0, 0);
-            float big = 0.0f, sum[G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) sum[g] = 0.0f;
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const uint32_t xs[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    big = fmaxf(big, fmaxf(fabsf(bf16_lo(xs[e])), fabsf(bf16_hi(xs[e]))));
-                    sum[w / WG] += bf16_lo(xs[e]) + bf16_hi(xs[e]);
-                }
-            }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-            }
-            // the largest q of the row to [2^13, 2^14)
-            const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 115);
-            const float up = __uint_as_float((uint32_t)(127 + 13 - ex) << 23);
-            const float down = __uint_as_float((uint32_t)(127 + 11 + ex) << 23);    // 2^24 / up
-#pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float f[8] = {bf16_lo(x[w].x), bf16_hi(x[w].x), bf16_lo(x[w].y), bf16_hi(x[w].y),
-                                    bf16_lo(x[w].z), bf16_hi(x[w].z), bf16_lo(x[w].w), bf16_hi(x[w].w)};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float s = e & 1 ? up * 0.0625f : up;
-                    qb[nt][w][e] = pack_f16(f[e] * s, f[e + 4] * s);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int src = (2 * t4 + e) * 4;
-                kf[nt][e] = __shfl_sync(0xffffffffu, down, src);
-#pragma unroll
-                for (int g = 0; g < G; ++g) qs[nt][e][g] = __shfl_sync(0xffffffffu, sum[g], src) / kf[nt][e];
-            }
-        }
-    };
     auto reset = [&]() {
+        const float2 zero2 = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < MT; ++c)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[c][nt][0] = acc[c][nt][1] = acc[c][nt][2] = acc[c][nt][3] = 0.0f;
+            for (int nt = 0; nt < NT; ++nt) acc[c][nt][0] = acc[c][nt][1] = zero2;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = make_float2(-kQ4NoMax, -kQ4NoMax);
+            thr[nt] = make_float2(-INFINITY, -INFINITY);
+            l[nt] = zero2;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                m[nt][e] = -INFINITY;
-                l[nt][e] = 0.0f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) zac[nt][e][g] = 0.0f;
-            }
+            for (int g = 0; g < G; ++g) zac[nt][g] = zero2;
+        }
         beta = 1.0f;
-        cap_step = 0.0f;
+        cap_meta = 16;                               // a step above zero
         since = 0;
+    };
+    auto over_rows = [&](float2 v) {                 // the sum over the lanes of a column
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        return v;
     };
     // takes sum w zero out of the accumulators
     auto recentre = [&]() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int g = 0; g < G; ++g) {
+                const float2 z = over_rows(zac[nt][g]);
+                zac[nt][g] = make_float2(0.0f, 0.0f);
+                const float lo = -5.9604644775390625e-8f, hi = -9.5367431640625e-7f;     // -2^-24, -2^-20
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    float z = zac[nt][e][g];
-                    z += __shfl_xor_sync(0xffffffffu, z, 4);
-                    z += __shfl_xor_sync(0xffffffffu, z, 8);
-                    z += __shfl_xor_sync(0xffffffffu, z, 16);
-                    zac[nt][e][g] = 0.0f;
-#pragma unroll
-                    for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
-                        acc[c][nt][e] = fmaf(z, -5.9604644775390625e-8f, acc[c][nt][e]);             // 2^-24
-                        acc[c][nt][2 + e] = fmaf(z, -9.5367431640625e-7f, acc[c][nt][2 + e]);        // 2^-20
-                    }
+                for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
+                    acc[c][nt][0] = ffma2(z, make_float2(lo, lo), acc[c][nt][0]);
+                    acc[c][nt][1] = ffma2(z, make_float2(hi, hi), acc[c][nt][1]);
                 }
+            }
         since = 0;
     };
     // the end of a sequence or of the share: join the SUB warps of the head, write the partial
     auto flush_partial = [&](int vb, int n) {
         recentre();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float s = l[nt][e];
-                s += __shfl_xor_sync(0xffffffffu, s, 4);
-                s += __shfl_xor_sync(0xffffffffu, s, 8);
-                s += __shfl_xor_sync(0xffffffffu, s, 16);
-                l[nt][e] = s;
-            }
-        const float back = 1.0f / beta;              // a power of two
-#pragma unroll
-        for (int c = 0; c < MT; ++c)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[c][nt][e] = acc[c][nt][e] * (e < 2 ? 16777216.0f : 1048576.0f) * back;
-        constexpr int FL = MT * NT * 4 + NT * 4;     // floats a lane exchanges
+        for (int nt = 0; nt < NT; ++nt) l[nt] = over_rows(l[nt]);
+        constexpr int FL = MT * NT * 2 + NT * 2 + 1; // pairs a lane exchanges
         const int slots = (SUB + 1) / 2;
-        float* mine = mrg + (long long)h * slots * 32 * FL;
+        float2* mine = reinterpret_cast<float2*>(mrg) + h * slots * 32 * FL;
         int width = 1;
         while (width < SUB) width <<= 1;
         for (int st = width / 2; st > 0; st >>= 1) {
             if (sub >= st && sub < 2 * st) {
-                float* x = mine + (sub - st) * 32 * FL + lane;
-                int i = 0;
+                float2* x = mine + (sub - st) * 32 * FL + lane;
 #pragma unroll
                 for (int c = 0; c < MT; ++c)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) x[32 * i++] = acc[c][nt][e];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        x[32 * i++] = m[nt][e];
-                        x[32 * i++] = l[nt][e];
+                    for (int nt = 0; nt < NT; ++nt) {
+                        x[32 * (c * NT + nt) * 2] = acc[c][nt][0];
+                        x[32 * ((c * NT + nt) * 2 + 1)] = acc[c][nt][1];
                     }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    x[32 * (MT * NT + nt) * 2] = m[nt];
+                    x[32 * ((MT * NT + nt) * 2 + 1)] = l[nt];
+                }
+                x[32 * (FL - 1)] = make_float2(beta, 0.0f);
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + h), "r"(32 * SUB) : "memory");
             if (sub < st && sub + st < SUB) {
-                const float* x = mine + sub * 32 * FL + lane;
+                const float2* x = mine + sub * 32 * FL + lane;
+                const float beta2 = x[32 * (FL - 1)].x, nb = fminf(beta, beta2);     // the larger steps' unit
+                const float r1 = nb / beta, r2 = nb / beta2;
+                beta = nb;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 m2 = x[32 * (MT * NT + nt) * 2], l2 = x[32 * ((MT * NT + nt) * 2 + 1)];
+                    const float2 mn = make_float2(fminf(m[nt].x, m2.x), fminf(m[nt].y, m2.y));
+                    float2 f1 = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
+                    float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
+                    m[nt] = mn;
+                    l[nt] = ffma2(l[nt], f1, fmul2(l2, f2));
+                    f1 = fmul2(f1, make_float2(r1, r1));
+                    f2 = fmul2(f2, make_float2(r2, r2));
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float m2 = x[32 * (MT * NT * 4 + (nt * 2 + e) * 2)];
-                        const float l2 = x[32 * (MT * NT * 4 + (nt * 2 + e) * 2 + 1)];
-                        const float mn = fmaxf(m[nt][e], m2);
-                        const float f1 = mn == -INFINITY ? 1.0f : ex2(m[nt][e] - mn);
-                        const float f2 = mn == -INFINITY ? 1.0f : ex2(m2 - mn);
-                        m[nt][e] = mn;
-                        l[nt][e] = l[nt][e] * f1 + l2 * f2;
+                    for (int c = 0; c < MT; ++c)
 #pragma unroll
-                        for (int c = 0; c < MT; ++c) {
-                            acc[c][nt][e] = acc[c][nt][e] * f1 + x[32 * ((c * NT + nt) * 4 + e)] * f2;
-                            acc[c][nt][2 + e] = acc[c][nt][2 + e] * f1 + x[32 * ((c * NT + nt) * 4 + 2 + e)] * f2;
-                        }
-                    }
+                        for (int y = 0; y < 2; ++y)
+                            acc[c][nt][y] = ffma2(acc[c][nt][y], f1, fmul2(x[32 * ((c * NT + nt) * 2 + y)], f2));
+                }
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + h), "r"(32 * SUB) : "memory");
         }
         if (sub != 0) return;
+        const float back = 64.0f / beta;             // a power of two, within range for every step
         const long long row0 = (((long long)blockIdx.x + vb) * HB + h) * (8 * NT);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -751,104 +897,168 @@ __global__ void __launch_bounds__(NT == 1 ? 544 : 288, 1) q4_attn_kernel(const Q
             for (int e = 0; e < 2; ++e) {
                 const int row = nt * 8 + 2 * t4 + e;
                 if (row >= n * a.group) continue;
-                const float s = l[nt][e];
+                const float s = e ? l[nt].y : l[nt].x;
                 const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
+                const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
                 float* rp = a.o_part + (row0 + row) * D;
 #pragma unroll
                 for (int c = 0; c < MT; ++c) {
-                    rp[16 * c + r8] = acc[c][nt][e] * inv;
-                    rp[16 * c + 8 + r8] = acc[c][nt][2 + e] * inv;
+                    rp[16 * c + r8] = (e ? acc[c][nt][0].y : acc[c][nt][0].x) * lo * back;
+                    rp[16 * c + 8 + r8] = (e ? acc[c][nt][1].y : acc[c][nt][1].x) * hi * back;
                 }
                 if (r8 == 0)
-                    a.lse_part[row0 + row] = s > 0.0f ? (m[nt][e] + log2f(s)) * kLn2 : s == s ? -INFINITY : s;
+                    a.lse_part[row0 + row] = s > 0.0f ? (log2f(s) - (e ? m[nt].y : m[nt].x)) * kLn2 : s == s ? -INFINITY : s;
             }
     };
     bool ok = true;
-    int i = sub;                                     // this warp's next page of the share
-    for (int seg = 0; seg < npages;) {
-        const long long vg = p0 + seg;
-        const int hb = (int)(vg / P), g0 = (int)(vg % P);
-        const int b = seq_of(g0);
-        const int seg_end = (int)min((long long)npages, (long long)hb * P + prefix[b + 1] - p0);
+    int i = sub, st = sub;                           // this warp's next page of the share, and its stage
+    uint32_t ph = 0;
+    while (st >= NS) {
+        st -= NS;
+        ph ^= 1;
+    }
+    const uint8_t* kbase = smem + h * C::TILE + r8 * (D / 2) + t4 * W * 4;
+    const uint8_t* vbase = smem + (HB + h) * C::TILE + lane * W * 4;
+    const uint8_t* mbase = smem + 2 * HB * C::TILE + h * C::META + r8 * G * 2;
+    // raw scores of a page's keys r8 and r8 + 8 against the tile's columns
+    auto scores = [&](int so, float2 (&sc)[NT][2]) {
+        uint32_t k0[W], k1[W], km0[G], km1[G];
+        load_words<W>(kbase + so, k0);
+        load_words<W>(kbase + so + 4 * D, k1);
+        load_metas<G>(mbase + so, km0);
+        load_metas<G>(mbase + so + 16 * G, km1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float raw[NT][4], raw2[NT][4];
+#pragma unroll
+            for (int w = g * WG; w < (g + 1) * WG; ++w) {
+                const uint32_t lo[4] = {k0[w] & 0x000f000fu, k1[w] & 0x000f000fu, k0[w] & 0x00f000f0u, k1[w] & 0x00f000f0u};
+                const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
+                const uint32_t hi[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + (nt * W + w) * 512);
+                    if (w == g * WG) {
+                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
+                        q4_mma_first(raw2[nt], hi, qw.z, qw.w);
+                    } else {
+                        q4_mma(raw[nt], lo, qw.x, qw.y);
+                        q4_mma(raw2[nt], hi, qw.z, qw.w);
+                    }
+                }
+            }
+            const float s0 = q4_step(km0[g]), s1 = q4_step(km1[g]), z0 = q4_zero(km0[g]), z1 = q4_zero(km1[g]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float2 y0 = ffma2(make_float2(z0, z0), qs[nt][g],
+                                        fadd2(make_float2(raw[nt][0], raw[nt][1]), make_float2(raw2[nt][0], raw2[nt][1])));
+                const float2 y1 = ffma2(make_float2(z1, z1), qs[nt][g],
+                                        fadd2(make_float2(raw[nt][2], raw[nt][3]), make_float2(raw2[nt][2], raw2[nt][3])));
+                sc[nt][0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[nt][0]);
+                sc[nt][1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[nt][1]);
+            }
+        }
+    };
+    int turn = 0;                                    // sequences of the share so far
+    Place place = start;
+    for (int seg = 0; seg < npages; ++turn) {
+        if (turn) place = next_place(place);
+        const int hb = place.hb, b = place.b, seg_end = place.end, g0 = p0 + seg - hb * P;
         const int L = lenv[b], n = queries(b);
         // first key of the share's page `seg`
         const int key0 = (g0 - prefix[b] + q4_first_key(L, n, a.window) / kPageRows) * kPageRows;
-        load_q(b, n, (hb * HB + h) * a.group);
         reset();
+        if (turn == 0) {
+            prepare(0, hb, b, warp, HB * SUB);
+            asm volatile("bar.sync 15, %0;" ::"r"(32 * HB * SUB) : "memory");
+        } else if (ok) {
+            ok = mbar_wait(&qfull[turn & 1], (turn >> 1 & 1) ^ (turn & 1 ^ 1), kErrQ4Full);
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        {
+            const uint8_t* q = qarea + (turn & 1) * QB;
+            qb = (uint32_t)(qarea - smem) + (turn & 1) * QB + (h * NT * W * 32 + lane) * 16;
+            const float* rows = reinterpret_cast<const float*>(q + HB * NT * W * 512) + h * C::QROWS * 8 * NT + 2 * t4;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                kf[nt] = *reinterpret_cast<const float2*>(rows + 8 * nt);
+#pragma unroll
+                for (int g = 0; g < G; ++g) qs[nt][g] = *reinterpret_cast<const float2*>(rows + (1 + g) * 8 * NT + 8 * nt);
+            }
+        }
         // pages whose keys every query sees: key0 of the page in [all_lo, all_hi]
         const int all_hi = (a.causal ? L - n : L - 1) - (kPageRows - 1);
         const int all_lo = a.window >= 0 ? L - 1 - a.window : 0;
-        for (; i < seg_end; i += SUB) {
-            const int st = i % NS;
-            if (ok) {
-                ok = mbar_wait(&full[st], (i / NS) & 1, kErrQ4Full);
-                ok = __all_sync(0xffffffffu, ok);
+        // waits for this warp's next page (and the one after); their stages go to `at`
+        auto take = [&](int (&at)[NP]) {
+            const bool two = NP > 1 && i + SUB < seg_end;
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                if (x == 0 || two) {
+                    if (ok) {
+                        ok = mbar_wait(&full[st], ph, kErrQ4Full);
+                        ok = __all_sync(0xffffffffu, ok);
+                    }
+                    at[x] = st;
+                    st += SUB;
+                    while (st >= NS) {
+                        st -= NS;
+                        ph ^= 1;
+                    }
+                } else {
+                    at[x] = at[0];                               // no second page: masked below
+                }
             }
-            if (ok) {
-                const int tok0 = key0 + (i - seg) * kPageRows;
-                const uint8_t* stage = smem + st * SB;
-                const uint32_t* kt = reinterpret_cast<const uint32_t*>(stage + h * C::TILE) + r8 * (D / 8) + t4 * W;
-                const uint32_t* vt = reinterpret_cast<const uint32_t*>(stage + (HB + h) * C::TILE) + lane * W;
-                const uint16_t* km = reinterpret_cast<const uint16_t*>(stage + 2 * HB * C::TILE + h * C::META) + r8 * G;
-                const uint16_t* vm = km + HB * C::META / 2;
-                uint32_t k0[W], k1[W];
+            i += two ? 2 * SUB : SUB;
+            return two;
+        };
+        int at[NP], next[NP];
+        float2 sc[NP][NT][2], sn[NP][NT][2];
+        int tok0 = key0 + (i - seg) * kPageRows;                 // first key of the first page
+        bool live = i < seg_end, two = false;
+        if (live) {
+            two = take(at);
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    k0[w] = kt[w];
-                    k1[w] = kt[D + w];
+            for (int x = 0; x < NP; ++x) scores(at[x] * SB, sc[x]);
+        }
+        while (live) {
+            // the pages after these: their scores are computed beside these pages' softmax
+            const bool more = i < seg_end;
+            const int tok_n = key0 + (i - seg) * kPageRows;
+            bool two_n = false;
+            if (more) {
+                two_n = take(next);
+            } else {
+#pragma unroll
+                for (int x = 0; x < NP; ++x) next[x] = at[x];    // (computed and not used)
+            }
+            uint32_t vm0[NP][G], vm1[NP][G];
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                load_metas<G>(mbase + at[x] * SB + HB * C::META, vm0[x]);
+                load_metas<G>(mbase + at[x] * SB + HB * C::META + 16 * G, vm1[x]);
+            }
+            if (capped) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float b0 = kf[nt].x * kLn2, b1 = kf[nt].y * kLn2;             // to natural units
+                    const float i0 = b0 / a.softcap, i1 = b1 / a.softcap, o0 = a.softcap / b0, o1 = a.softcap / b1;
+#pragma unroll
+                    for (int x = 0; x < NP; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            sc[x][nt][y] = make_float2(softcap_raw(sc[x][nt][y].x, i0, o0), softcap_raw(sc[x][nt][y].y, i1, o1));
                 }
-                float sc[NT][4];
+            }
+            if ((NP > 1 && !two) || tok0 + (NP - 1) * SUB * kPageRows > all_hi || tok0 < all_lo) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    float raw[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) raw[nt][0] = raw[nt][1] = raw[nt][2] = raw[nt][3] = 0.0f;
-#pragma unroll
-                    for (int w = g * WG; w < (g + 1) * WG; ++w) {
-                        const uint32_t lo[4] = {k0[w] & 0x000f000fu, k1[w] & 0x000f000fu, k0[w] & 0x00f000f0u,
-                                                k1[w] & 0x00f000f0u};
-                        const uint32_t s0 = k0[w] >> 8, s1 = k1[w] >> 8;
-                        const uint32_t hi[4] = {s0 & 0x000f000fu, s1 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x00f000f0u};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16_16816(raw[nt], lo, qb[nt][w][0], qb[nt][w][1]);
-                            mma_f16_16816(raw[nt], hi, qb[nt][w][2], qb[nt][w][3]);
-                        }
-                    }
-                    const uint32_t m0 = km[g], m1 = km[8 * G + g];
-                    const float s0 = q4_step(m0), s1 = q4_step(m1), z0 = -q4_zero(m0), z1 = -q4_zero(m1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            sc[nt][e] = fmaf(fmaf(z0, qs[nt][e][g], raw[nt][e]), s0, sc[nt][e]);
-                            sc[nt][2 + e] = fmaf(fmaf(z1, qs[nt][e][g], raw[nt][2 + e]), s1, sc[nt][2 + e]);
-                        }
-                }
-                // to log2 units
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = sc[nt][e] * (kf[nt][e & 1] * a.scale);
-                        if (capped) x = a.softcap * tanh_ex2(x / a.softcap);
-                        sc[nt][e] = x * kLog2e;
-                    }
-                float vs[2][G], vz[2][G];
-#pragma unroll
-                for (int g = 0; g < G; ++g) {
-                    const uint32_t m0 = vm[g], m1 = vm[8 * G + g];
-                    vs[0][g] = q4_step(m0), vs[1][g] = q4_step(m1), vz[0][g] = q4_zero(m0), vz[1][g] = q4_zero(m1);
-                }
-                if (tok0 > all_hi || tok0 < all_lo) {
+                for (int x = 0; x < NP; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const int key = tok0 + r8 + 8 * y;
+                        const int key = x == 0 || two ? tok0 + x * SUB * kPageRows + r8 + 8 * y : L;
                         if (key >= L) {                // not data of the sequence
 #pragma unroll
-                            for (int g = 0; g < G; ++g) vs[y][g] = vz[y][g] = 0.0f;
+                            for (int g = 0; g < G; ++g) (y ? vm1 : vm0)[x][g] = 0;
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -857,158 +1067,230 @@ __global__ void __launch_bounds__(NT == 1 ? 544 : 288, 1) q4_attn_kernel(const Q
                                 const int tok = (nt * 8 + 2 * t4 + e) / a.group;
                                 const int last = a.causal ? L - n + tok : L - 1;
                                 if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
-                                    sc[nt][2 * y + e] = -INFINITY;
+                                    (e ? sc[x][nt][y].y : sc[x][nt][y].x) = -INFINITY;
                             }
                     }
+            }
+            // does a score exceed its row's maximum by the slack, or a step the range?
+            uint32_t top = 0;
+#pragma unroll
+            for (int x = 0; x < NP; ++x)
+#pragma unroll
+                for (int g = 0; g < G; ++g) top = max(top, max(vm0[x][g], vm1[x][g]));
+            bool over = top >= cap_meta;
+            float2 mx[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
+                if (NP > 1) {
+                    mx[nt].x = fmax3(mx[nt].x, sc[NP - 1][nt][0].x, sc[NP - 1][nt][1].x);
+                    mx[nt].y = fmax3(mx[nt].y, sc[NP - 1][nt][0].y, sc[NP - 1][nt][1].y);
                 }
-                // does a score exceed its row's maximum by the slack, or a step the range?
-                bool over = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        over = over || fmaxf(sc[nt][e], sc[nt][2 + e]) > m[nt][e] + kQ4Slack;
-                float top = 0.0f;
-#pragma unroll
-                for (int g = 0; g < G; ++g) top = fmaxf(top, fmaxf(vs[0][g], vs[1][g]));
-                over = over || (top >= cap_step && top > 0.0f && top < INFINITY);
-                if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    float resc = 1.0f;
-                    if (top >= cap_step && top > 0.0f && top < INFINITY) {
-                        // 2^ex <= top < 2^(ex + 1): beta puts it below 2^7
-                        const int ex = (int)(__float_as_uint(top) >> 23) - 127;
+                over = over || mx[nt].x > thr[nt].x || mx[nt].y > thr[nt].y;
+            }
+            if (__any_sync(0xffffffffu, over)) {
+                top = __reduce_max_sync(0xffffffffu, top);
+                float resc = 1.0f;
+                if (top >= cap_meta) {
+                    // 2^ex <= step < 2^(ex + 1): beta puts it below 2^7 (a NaN needs none)
+                    const int ex = (int)(top >> 7) - 127;
+                    if (ex < 128) {
                         const float nb = __uint_as_float((uint32_t)(127 + 6 - ex) << 23);
-                        cap_step = ex < 127 ? __uint_as_float((uint32_t)(127 + 1 + ex) << 23) : INFINITY;
                         resc = nb / beta;
                         beta = nb;
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float mx = fmaxf(sc[nt][e], sc[nt][2 + e]);
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                            const float mn = fmaxf(m[nt][e], mx);
-                            const float al = mn == -INFINITY ? 1.0f : ex2(m[nt][e] - mn);
-                            m[nt][e] = mn;
-                            l[nt][e] *= al;
-                            const float f = al * resc;
-#pragma unroll
-                            for (int g = 0; g < G; ++g) zac[nt][e][g] *= f;
-#pragma unroll
-                            for (int c = 0; c < MT; ++c) {
-                                acc[c][nt][e] *= f;
-                                acc[c][nt][2 + e] *= f;
-                            }
-                        }
+                    cap_meta = (uint32_t)(ex + 128) << 7;
                 }
-                float p[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float2 y = mx[nt];
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
+                        y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
+                    }
+                    const float2 mn = make_float2(fminf(m[nt].x, -y.x * kf[nt].x), fminf(m[nt].y, -y.y * kf[nt].y));
+                    const float2 al = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
+                    m[nt] = mn;
+                    thr[nt].x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf[nt].x;
+                    thr[nt].y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf[nt].y;
+                    l[nt] = fmul2(l[nt], al);
+                    const float2 f = make_float2(al.x * resc, al.y * resc);
+#pragma unroll
+                    for (int g = 0; g < G; ++g) zac[nt][g] = fmul2(zac[nt][g], f);
+#pragma unroll
+                    for (int c = 0; c < MT; ++c) {
+                        acc[c][nt][0] = fmul2(acc[c][nt][0], f);
+                        acc[c][nt][1] = fmul2(acc[c][nt][1], f);
+                    }
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                float2 p[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float mu = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
-                        p[nt][e] = ex2(sc[nt][e] - mu);
-                        p[nt][2 + e] = ex2(sc[nt][2 + e] - mu);
-                        l[nt][e] += p[nt][e] + p[nt][2 + e];
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 d = ffma2(sc[x][nt][y], kf[nt], m[nt]);
+                        p[nt][y] = make_float2(ex2(d.x), ex2(d.y));
+                        l[nt] = fadd2(l[nt], p[nt][y]);
                     }
+                scores(next[x] * SB, sn[x]);
                 uint32_t v0[W], v1[W];
-#pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    v0[w] = vt[w];
-                    v1[w] = vt[32 * W + w];
-                }
+                load_words<W>(vbase + at[x] * SB, v0);
+                load_words<W>(vbase + at[x] * SB + 128 * W, v1);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float w0 = vs[0][g] * beta, w1 = vs[1][g] * beta;
+                    const float w0 = q4_step(vm0[x][g]) * beta, w1 = q4_step(vm1[x][g]) * beta;
+                    const float z0 = q4_zero(vm0[x][g]), z1 = q4_zero(vm1[x][g]);
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float x0 = p[nt][0] * w0, x1 = p[nt][1] * w0, x2 = p[nt][2] * w1, x3 = p[nt][3] * w1;
-                        zac[nt][0][g] = fmaf(x0, vz[0][g], fmaf(x2, vz[1][g], zac[nt][0][g]));
-                        zac[nt][1][g] = fmaf(x1, vz[0][g], fmaf(x3, vz[1][g], zac[nt][1][g]));
-                        pb[nt][0] = movmatrix_trans(pack_f16(x0, x1));
-                        pb[nt][1] = movmatrix_trans(pack_f16(x2, x3));
+                        const float2 x0 = fmul2(p[nt][0], make_float2(w0, w0)), x1 = fmul2(p[nt][1], make_float2(w1, w1));
+                        zac[nt][g] = ffma2(x0, make_float2(z0, z0), ffma2(x1, make_float2(z1, z1), zac[nt][g]));
+                        pb[nt][0] = movmatrix_trans(pack_f16(x0.x, x0.y));
+                        pb[nt][1] = movmatrix_trans(pack_f16(x1.x, x1.y));
                     }
 #pragma unroll
                     for (int w = g * WG; w < (g + 1) * WG; ++w) {
                         const uint32_t lo[4] = {v0[w] & 0x000f000fu, v0[w] & 0x00f000f0u, v1[w] & 0x000f000fu,
                                                 v1[w] & 0x00f000f0u};
-                        const uint32_t s0 = v0[w] >> 8, s1 = v1[w] >> 8;
-                        const uint32_t hi[4] = {s0 & 0x000f000fu, s0 & 0x00f000f0u, s1 & 0x000f000fu, s1 & 0x00f000f0u};
+                        const uint32_t y0 = v0[w] >> 8, y1 = v1[w] >> 8;
+                        const uint32_t hi[4] = {y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16_16816(acc[2 * w][nt], lo, pb[nt][0], pb[nt][1]);
-                            mma_f16_16816(acc[2 * w + 1][nt], hi, pb[nt][0], pb[nt][1]);
+                            q4_mma2(acc[2 * w][nt], lo, pb[nt][0], pb[nt][1]);
+                            q4_mma2(acc[2 * w + 1][nt], hi, pb[nt][0], pb[nt][1]);
                         }
                     }
                 }
-                if (++since == kQ4Recentre) recentre();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[st]);
+            if (lane == 0) {
+                mbar_arrive(&empty[at[0]]);
+                if (two) mbar_arrive(&empty[at[NP - 1]]);
+            }
+            since += NP;
+            if (since >= kQ4Recentre) recentre();
+            live = more;
+            two = two_n;
+            tok0 = tok_n;
+#pragma unroll
+            for (int x = 0; x < NP; ++x) {
+                at[x] = next[x];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sc[x][nt][0] = sn[x][nt][0];
+                    sc[x][nt][1] = sn[x][nt][1];
+                }
+            }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qempty[turn & 1]);
         flush_partial(hb * a.B + b, n);
         seg = seg_end;
     }
 }
 
-// Joins the partials: a warp per output row.  The partials of sequence b and head
-// block hb sit in slots c + hb B + b for the CTAs c whose shares covered it.
+// Joins the partials: a.wpr warps per output row.  The partials of sequence b and
+// head block hb sit in slots c + hb B + b for the CTAs c whose shares covered it.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     constexpr int V = D / 32;            // columns of a lane
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    constexpr int N = 8;                 // partials whose loads are in flight together
+    __shared__ float part[8][32 * V + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % a.wpr;        // this warp's share of the row's partials
+    const long long w = (long long)blockIdx.x * (8 / a.wpr) + warp / a.wpr;
     const int per = a.max_q * a.Hq;      // rows of a sequence
-    if (w >= (long long)a.B * per) return;
-    const int b = (int)(w / per), tok = (int)(w % per) / a.Hq, hq = (int)(w % per) % a.Hq;
+    bool live = w < (long long)a.B * per;
+    const int b = live ? (int)(w / per) : 0, tok = live ? (int)(w % per) / a.Hq : 0, hq = live ? (int)(w % per) % a.Hq : 0;
     const long long q0 = a.cu_q ? __ldg(&a.cu_q[b]) : b;
-    if (a.cu_q && tok >= __ldg(&a.cu_q[b + 1]) - q0) return;
+    if (a.cu_q) live = live && tok < __ldg(&a.cu_q[b + 1]) - q0;
     const int hkv = hq / a.group, hb = hkv / a.HB, h = hkv % a.HB;
     const int row = tok * a.group + hq % a.group;
-    const long long P = a.meta[a.B], ppc = max(a.meta[a.B + 1], 1);
-    const long long pb = hb * P + a.meta[b], pe = hb * P + a.meta[b + 1];
-    const long long c0 = pb / ppc;
-    const int ns = pe > pb ? (int)((pe - 1) / ppc - c0 + 1) : 0;
-    const long long first = ((c0 + (long long)hb * a.B + b) * a.HB + h) * (8 * NT) + row;
-    const long long step = (long long)a.HB * 8 * NT;
-    float M = -INFINITY;
-    bool nan = false;
-    for (int s = lane; s < ns; s += 32) {
-        const float x = a.lse_part[first + s * step];
-        nan = nan || x != x;
-        M = fmaxf(M, x);
+    // The shares follow from the lengths alone: worked out while the attention kernel still
+    // runs (which began after whatever wrote the lengths had ended).
+    int PC = 0, cb = 0, mine = 0;
+    for (int s = lane; s < a.B; s += 32) {
+        const int pages = q4_pages(a, s), c = pages > 0 ? pages + kQ4Switch : 0;
+        PC += c;
+        cb += s < b ? c : 0;
+        mine += s == b ? pages : 0;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    nan = __any_sync(0xffffffffu, nan);
-    float sum = 0.0f, acc[V];
+    PC = __reduce_add_sync(0xffffffffu, PC);
+    cb = __reduce_add_sync(0xffffffffu, cb);
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    const int share = q4_share(PC, a);
+    const int c0 = (hb * PC + cb + kQ4Switch) / share;            // the CTAs of its first and last page
+    const int ns = live && mine > 0 ? (hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1 : 0;
+    const long long first = (((long long)c0 + hb * a.B + b) * a.HB + h) * (8 * NT) + row;
+    const long long step = (long long)a.HB * 8 * NT * a.wpr;      // rows between this warp's partials
+    float M = -INFINITY, sum = 0.0f, acc[V];
+    bool nan = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int s = 0; s < ns; ++s) {
-            const float f = ex2((a.lse_part[first + s * step] - M) * kLog2e);
-            sum += f;
-            const float* src = a.o_part + (first + s * step) * D + lane * V;
-            float x[V];
-            if constexpr (V == 4) {
-                const float4 t = *reinterpret_cast<const float4*>(src);
-                x[0] = t.x, x[1] = t.y, x[2] = t.z, x[3] = t.w;
-            } else {
-                const float2 t = *reinterpret_cast<const float2*>(src);
-                x[0] = t.x, x[1] = t.y;
-            }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int s0 = sub; s0 < ns; s0 += N * a.wpr) {
+        const long long at = first + (long long)s0 / a.wpr * step + (long long)sub * a.HB * 8 * NT;
+        float x[N], y[N][V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(f, x[v], acc[v]);
+        for (int i = 0; i < N; ++i) {
+            const bool has = s0 + i * a.wpr < ns;
+            x[i] = has ? a.lse_part[at + i * step] : -INFINITY;
+            const float* src = a.o_part + (at + i * step) * D + lane * V;
+            if constexpr (V == 4) {
+                const float4 f = has ? *reinterpret_cast<const float4*>(src) : make_float4(0, 0, 0, 0);
+                y[i][0] = f.x, y[i][1] = f.y, y[i][2] = f.z, y[i][3] = f.w;
+            } else {
+                const float2 f = has ? *reinterpret_cast<const float2*>(src) : make_float2(0, 0);
+                y[i][0] = f.x, y[i][1] = f.y;
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            nan = nan || x[i] != x[i];
+            mn = fmaxf(mn, x[i]);
+        }
+        if (mn == -INFINITY) continue;
+        const float al = ex2((M - mn) * kLog2e);
+        M = mn;
+        sum *= al;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= al;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float f = ex2((x[i] - mn) * kLog2e);
+            sum += f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(f, y[i][v], acc[v]);
         }
     }
+    if (a.wpr > 1) {
+        // the row's warps through shared memory, in order (the sum does not depend on their speed)
+#pragma unroll
+        for (int v = 0; v < V; ++v) part[warp][v * 32 + lane] = acc[v];
+        if (lane == 0) {
+            part[warp][32 * V] = nan ? NAN : M;
+            part[warp][32 * V + 1] = sum;
+        }
+        __syncthreads();
+        if (sub != 0) return;
+        for (int s = 1; s < a.wpr; ++s) {
+            const float m2 = part[warp + s][32 * V];
+            if (m2 != m2) nan = true;
+            const float mn = fmaxf(M, m2);
+            if (mn == -INFINITY) continue;
+            const float f1 = ex2((M - mn) * kLog2e), f2 = ex2((m2 - mn) * kLog2e);
+            M = mn;
+            sum = sum * f1 + part[warp + s][32 * V + 1] * f2;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = acc[v] * f1 + part[warp + s][v * 32 + lane] * f2;
+        }
+    }
+    if (!live) return;
     const float inv = nan ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
     __nv_bfloat16* dst = a.o + ((q0 + tok) * a.Hq + hq) * D + lane * V;
     if constexpr (V == 4)
