@@ -67,11 +67,32 @@ void q4_split(int Hkv, int NT, int* HB, int* SUB) {
     *SUB = warps / best;
 }
 
-size_t q4_workspace(int B, int Hkv, int D, int NT, int sms) {
+// How the partial results of a call are laid out: `slots` of (CTA, sequence and block of
+// heads), each of `parts` for the warps of a head.  A change of sequence is what a CTA's
+// warps can do without meeting (a meeting costs 1.5 us); but where few sequences are
+// spread over many CTAs the combine kernel would read SUB times as many partials (at 148
+// CTAs a sequence 2.5 us against 5), and changes are few.
+struct Q4Parts {
+    size_t slots;
+    int spread, parts;
+};
+Q4Parts q4_parts(int B, int nhb, int SUB, int grid) {
+    Q4Parts p;
+    p.slots = (size_t)grid + (size_t)nhb * B;
+    p.spread = grid / std::max(1, nhb * B);
+    p.parts = p.spread > 8 || p.slots > 2048 ? 1 : SUB;
+    return p;
+}
+
+size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
     int HB, SUB;
-    q4_split(Hkv, NT, &HB, &SUB);
-    const size_t slots = (size_t)sms + (size_t)(Hkv / HB) * B;
-    return slots * HB * 8 * NT * (D + 1) * sizeof(float);
+    q4_split(Hkv, rows > 8 ? 2 : 1, &HB, &SUB);
+    size_t most = 0;                       // (the grid may be smaller than the number of SMs)
+    for (int grid : {sms, std::min(sms, (Hkv / HB) * B * 9)}) {
+        const Q4Parts p = q4_parts(B, Hkv / HB, SUB, grid);
+        most = std::max(most, p.slots * p.parts);
+    }
+    return most * HB * rows * (D + 1) * sizeof(float);
 }
 
 bool q4_group_ok(int group_size, int D) {
@@ -94,8 +115,10 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     const long long bound = (long long)a.B * (a.max_blocks + kQ4Switch) * a.nhb;    // of the cost
     if (bound >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     const int grid = (int)std::min<long long>(sms, bound);
-    const size_t slots = (size_t)grid + (size_t)a.nhb * a.B;
-    const size_t rows = slots * a.HB * 8 * NT;
+    const Q4Parts p = q4_parts(a.B, a.nhb, a.SUB, grid);
+    a.rows = a.max_q * a.group;
+    a.parts = p.parts;
+    const size_t rows = p.slots * p.parts * a.HB * a.rows;
     if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
     if (workspace_bytes < rows * (D + 1) * sizeof(float))
         return ATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -108,14 +131,14 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     // a warp holds its pages and waits for the next ones: up to 4 SUB pages apart
     if (ns < 3 * a.SUB + 1) return ATTN_ERR_UNSUPPORTED;
     a.nstages = ns;
-    const int spread = grid / std::max(1, a.nhb * a.B);
-    a.wpr = spread <= 8 ? 1 : spread <= 16 ? 2 : spread <= 32 ? 4 : 8;
+    const int per_row = p.spread * p.parts;
+    a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;
     q4_attn_kernel<D, GS, NT><<<grid, 32 * (q4_warps(NT) + 4), C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st>>>(a);
     attn_status_t s = launch_status();
     if (s != ATTN_OK) return s;
     // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp
     const long long rows_out = (long long)a.B * a.max_q * a.Hq;
-    return launch_maybe_pdl(q4_combine_kernel<D, NT>, dim3((unsigned)((rows_out * a.wpr + 7) / 8)), dim3(256), 0, st, true, a);
+    return launch_maybe_pdl(q4_combine_kernel<D>, dim3((unsigned)((rows_out * a.wpr + 7) / 8)), dim3(256), 0, st, true, a);
 }
 
 template <int D, int GS>
@@ -384,7 +407,7 @@ attn_status_t attn_kv_gather_paged_q4(const void* k_cache, const void* v_cache, 
 
 size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 16) return 0;
-    return q4_workspace(B, Hkv, D, Hq / Hkv > 8 ? 2 : 1, current_sm_count_or(1024)) + 16;
+    return q4_workspace(B, Hkv, D, Hq / Hkv, current_sm_count_or(1024)) + 16;
 }
 
 attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_meta,
@@ -437,7 +460,7 @@ size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int 
     if (B <= 0 || max_seqlen_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || total_k < 0) return 0;
     const int group = Hq / Hkv;
     if (q4_fwd_streams(max_seqlen_q, group))
-        return q4_workspace(B, Hkv, D, max_seqlen_q * group > 8 ? 2 : 1, current_sm_count_or(1024)) + 16;
+        return q4_workspace(B, Hkv, D, max_seqlen_q * group, current_sm_count_or(1024)) + 16;
     return 2 * (size_t)std::max(total_k, 1) * Hkv * D * 2 + (size_t)(B + 1) * sizeof(int) + 16;
 }
 

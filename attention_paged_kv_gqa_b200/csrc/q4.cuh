@@ -406,7 +406,7 @@ constexpr int kQ4Recentre = 16;          // pages
 // Consumer warps of a CTA: as many as have the registers for 8 NT rows (and producer
 // warps for K, V, their metas and the queries).
 __host__ __device__ constexpr int q4_warps(int NT) { return NT == 1 ? 12 : 8; }
-constexpr int kQ4Switch = 4;             // pages that a change of sequence costs a CTA (for equal shares)
+constexpr int kQ4Switch = 13;            // pages that a change of sequence costs a CTA (for equal shares)
 constexpr float kQ4NoMax = -3.0e38f;     // the maximum before the first key (finite: differences with it stay numbers)
 
 struct Q4AttnArgs {
@@ -425,8 +425,10 @@ struct Q4AttnArgs {
     int causal;              // 0: every query sees every key
     int window;              // < 0: none
     float softcap;           // 0: none
-    float* o_part;           // [slots][HB][8 NT][D]
-    float* lse_part;         // [slots][HB][8 NT]
+    int rows;                // query rows of a KV head: group * max_q
+    int parts;               // partials of a (CTA, sequence): 1, its warps of a head joined in the CTA, or SUB
+    float* o_part;           // [slots][parts][HB][rows][D]
+    float* lse_part;         // [slots][parts][HB][rows]
     int grid;                // CTAs
     int nstages;
     int wpr;                 // combine: warps of a row (1, 2, 4 or 8)
@@ -845,7 +847,7 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         const int slots = (SUB + 1) / 2;
         float2* mine = reinterpret_cast<float2*>(mrg) + h * slots * 32 * FL;
         int width = 1;
-        while (width < SUB) width <<= 1;
+        while (width < SUB && a.parts == 1) width <<= 1;
         for (int st = width / 2; st > 0; st >>= 1) {
             if (sub >= st && sub < 2 * st) {
                 float2* x = mine + (sub - st) * 32 * FL + lane;
@@ -888,9 +890,9 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + h), "r"(32 * SUB) : "memory");
         }
-        if (sub != 0) return;
+        if (sub >= a.parts) return;
         const float back = 64.0f / beta;             // a power of two, within range for every step
-        const long long row0 = (((long long)blockIdx.x + vb) * HB + h) * (8 * NT);
+        const long long row0 = ((((long long)blockIdx.x + vb) * a.parts + sub) * HB + h) * a.rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1195,7 +1197,7 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
 
 // Joins the partials: a.wpr warps per output row.  The partials of sequence b and
 // head block hb sit in slots c + hb B + b for the CTAs c whose shares covered it.
-template <int D, int NT>
+template <int D>
 __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     constexpr int V = D / 32;            // columns of a lane
     constexpr int N = 8;                 // partials whose loads are in flight together
@@ -1224,16 +1226,16 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     mine = __reduce_add_sync(0xffffffffu, mine);
     const int share = q4_share(PC, a);
     const int c0 = (hb * PC + cb + kQ4Switch) / share;            // the CTAs of its first and last page
-    const int ns = live && mine > 0 ? (hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1 : 0;
-    const long long first = (((long long)c0 + hb * a.B + b) * a.HB + h) * (8 * NT) + row;
-    const long long step = (long long)a.HB * 8 * NT * a.wpr;      // rows between this warp's partials
+    const int ns = live && mine > 0 ? ((hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1) * a.parts : 0;
+    const long long first = (((long long)c0 + hb * a.B + b) * a.parts * a.HB + h) * a.rows + row;
+    const long long step = (long long)a.HB * a.rows * a.wpr;      // rows between this warp's partials
     float M = -INFINITY, sum = 0.0f, acc[V];
     bool nan = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int s0 = sub; s0 < ns; s0 += N * a.wpr) {
-        const long long at = first + (long long)s0 / a.wpr * step + (long long)sub * a.HB * 8 * NT;
+        const long long at = first + (long long)s0 * a.HB * a.rows;
         float x[N], y[N][V];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
