@@ -128,8 +128,8 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     using C = Q4Cfg<D, GS>;
     int ns = 0;
     while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= kQ4Smem) ++ns;
-    // a warp holds its pages and waits for the next ones: up to 4 SUB pages apart
-    if (ns < 3 * a.SUB + 1) return ATTN_ERR_UNSUPPORTED;
+    // a warp holds one page of a pair while it waits for the other, SUB pages on
+    if (ns < 2 * a.SUB) return ATTN_ERR_UNSUPPORTED;
     a.nstages = ns;
     const int per_row = p.spread * p.parts;
     a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;

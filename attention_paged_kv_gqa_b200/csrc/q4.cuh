@@ -1014,26 +1014,13 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
             i += two ? 2 * SUB : SUB;
             return two;
         };
-        int at[NP], next[NP];
-        float2 sc[NP][NT][2], sn[NP][NT][2];
-        int tok0 = key0 + (i - seg) * kPageRows;                 // first key of the first page
-        bool live = i < seg_end, two = false;
-        if (live) {
-            two = take(at);
+        int at[NP];
+        float2 sc[NP][NT][2];
+        while (i < seg_end) {
+            const int tok0 = key0 + (i - seg) * kPageRows;
+            const bool two = take(at);
 #pragma unroll
             for (int x = 0; x < NP; ++x) scores(at[x] * SB, sc[x]);
-        }
-        while (live) {
-            // the pages after these: their scores are computed beside these pages' softmax
-            const bool more = i < seg_end;
-            const int tok_n = key0 + (i - seg) * kPageRows;
-            bool two_n = false;
-            if (more) {
-                two_n = take(next);
-            } else {
-#pragma unroll
-                for (int x = 0; x < NP; ++x) next[x] = at[x];    // (computed and not used)
-            }
             uint32_t vm0[NP][G], vm1[NP][G];
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
@@ -1138,7 +1125,6 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
                         p[nt][y] = make_float2(ex2(d.x), ex2(d.y));
                         l[nt] = fadd2(l[nt], p[nt][y]);
                     }
-                scores(next[x] * SB, sn[x]);
                 uint32_t v0[W], v1[W];
                 load_words<W>(vbase + at[x] * SB, v0);
                 load_words<W>(vbase + at[x] * SB + 128 * W, v1);
@@ -1175,18 +1161,6 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
             }
             since += NP;
             if (since >= kQ4Recentre) recentre();
-            live = more;
-            two = two_n;
-            tok0 = tok_n;
-#pragma unroll
-            for (int x = 0; x < NP; ++x) {
-                at[x] = next[x];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[x][nt][0] = sn[x][nt][0];
-                    sc[x][nt][1] = sn[x][nt][1];
-                }
-            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&qempty[turn & 1]);
