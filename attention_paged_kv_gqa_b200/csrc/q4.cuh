@@ -30,27 +30,27 @@ enum : int { kErrQ4Rows = 531, kErrQ4Full = 541, kErrQ4Empty = 542 };
 
 // ---------------------------------------------------------------- quantiser
 struct Q4Group {
-    float step, inv;         // inv = 1 / step, or 0
+    float inv;               // 1 / step, or 0
     float zero;
     uint32_t meta;
 };
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+// Of two bf16 pairs the smaller and the larger elements; a NaN wins.
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
-// nearest(x / step) as an integer-valued float plus kQ4Magic (its low bits are
-// the integer), for |x / step| <= 16.  x has 8 significant bits and step 4, so
-// x / step lies either on a half-integer or further than 2^-12 from one: the sum
-// with 768, rounded to 2^-14, makes ties exact again whatever the rounding of
-// inv, and the second sum rounds them to even.
+// nearest(x / step) + kQ4Magic, for |x / step| <= 16.  x has 8 significant bits and
+// step 4, so x / step lies either on a half-integer or further than 2^-12 from one: the
+// sum with 768, rounded to 2^-14, makes ties exact again whatever the rounding of inv,
+// and the second sum rounds them to even.
 constexpr float kQ4Magic = 12582912.0f;     // 1.5 * 2^23
 __device__ __forceinline__ float q4_nearest(float x, float inv) {
     return __fadd_rn(__fmaf_rn(x, inv, 768.0f), kQ4Magic - 768.0f);
@@ -63,25 +63,30 @@ __device__ __forceinline__ Q4Group q4_group(float lo, float hi) {
     uint32_t bits = (__float_as_uint(s) + 0xfffffu) & 0xfff00000u;
     if (!(s < INFINITY)) bits = 0x7fc00000u;         // NaN or an infinity in the group
     else if (__uint_as_float(bits) < 7.888609052210118e-31f) bits = 0;   // 2^-100
-    g.step = __uint_as_float(bits);
     const bool live = bits != 0 && bits != 0x7fc00000u;
-    g.inv = live ? __frcp_rn(g.step) : 0.0f;
+    g.inv = live ? __frcp_rn(__uint_as_float(bits)) : 0.0f;
     g.zero = live ? __fsub_rn(q4_nearest(-lo, g.inv), kQ4Magic) : 0.0f;
     g.meta = (bits >> 16) | (uint32_t)(int)g.zero;
     return g;
 }
 
-// The codes of eight values, value i in nibble i.
-__device__ __forceinline__ uint32_t q4_codes(const float (&x)[8], const Q4Group& g) {
-    uint32_t w = 0;
+// The codes of eight values, value i in nibble i.  No code is below 0: the smallest value's
+// quotient rounds to minus zero.  The nibbles are put together as numbers (16-bit halves
+// are exact), and the sum with 2^23 leaves a half in the low bits.  (A NaN gives some code;
+// its group's step is NaN.)
+__device__ __forceinline__ uint32_t q4_codes(const float2 (&x)[4], const Q4Group& g) {
+    float c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        // (zero is added after the rounding, whose ties are to even; a NaN is held to the
-        // lower bound, its group's step is NaN)
-        const float v = fminf(fmaxf(__fadd_rn(q4_nearest(x[i], g.inv), g.zero), kQ4Magic), kQ4Magic + 15.0f);
-        w |= (__float_as_uint(v) & 15u) << (4 * i);
+    for (int i = 0; i < 4; ++i) {
+        const float2 n = fadd2(ffma2(x[i], make_float2(g.inv, g.inv), make_float2(768.0f, 768.0f)),
+                               make_float2(kQ4Magic - 768.0f, kQ4Magic - 768.0f));
+        const float2 v = fadd2(n, make_float2(g.zero - kQ4Magic, g.zero - kQ4Magic));
+        c[2 * i] = fminf(v.x, 15.0f);
+        c[2 * i + 1] = fminf(v.y, 15.0f);
     }
-    return w;
+    const float lo = fmaf(fmaf(fmaf(c[3], 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]) + 8388608.0f;
+    const float hi = fmaf(fmaf(fmaf(c[7], 16.0f, c[6]), 16.0f, c[5]), 16.0f, c[4]) + 8388608.0f;
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
 }
 
 __device__ __forceinline__ float q4_step(uint32_t meta) { return __uint_as_float((meta << 16) & 0xfff00000u); }
@@ -109,124 +114,151 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q4_kernel(const Rope
     const long long t = w / a.parts;
     const int part = (int)(w % a.parts);
     if (t >= a.total_new) return;
-    const NewToken nt = find_new_token(a, (int)t, lane == 0);
-    if (nt.b < 0) return;
     const int nrot = a.r.table ? a.r.rot / 16 : 0;
-
     const int nq = (a.Hq + HP - 1) / HP, nk = (a.Hkv + HV - 1) / HV;   // passes over q; over k, over v
+    constexpr int N = 4;                           // passes whose loads are in flight together
+
+    NewToken nt;
     {
         const int u = lane % U;
         const bool turns = u < nrot;
-        float c[8], s[8];
-        if (turns && part < nq) rope_angles(a.r, t, a.total_new, u, nt.pos, c, s);
         int ca, cb;
         rope_columns(a.r, u, &ca, &cb);
-        for (int i = part; i < nq; i += a.parts) {
-            const int h = i * HP + lane / U;
-            if (h >= a.Hq) continue;
-            const __nv_bfloat16* src = a.q.p + t * a.q.row + h * a.q.head;
-            uint4 xa = *reinterpret_cast<const uint4*>(src + ca), xb = *reinterpret_cast<const uint4*>(src + cb);
-            if (turns) rope_unit(xa, xb, c, s, a.r.interleaved);
-            __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + (t * a.Hq + h) * D;
-            *reinterpret_cast<uint4*>(dst + ca) = xa;
-            *reinterpret_cast<uint4*>(dst + cb) = xb;
+        uint4 xa[N], xb[N];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int h = (i0 + n * a.parts) * HP + lane / U;
+                if (h < a.Hq) {
+                    const __nv_bfloat16* src = a.q.p + t * a.q.row + h * a.q.head;
+                    xa[n] = *reinterpret_cast<const uint4*>(src + ca);
+                    xb[n] = *reinterpret_cast<const uint4*>(src + cb);
+                }
+            }
+        };
+        load(part);                                // in flight while the page and the angles are looked up
+        nt = find_new_token(a, (int)t, lane);
+        if (nt.b < 0) return;
+        RopeAngles g;
+        if (turns && part < nq) g = rope_angles(a.r, t, a.total_new, u, nt.pos);
+        for (int i0 = part; i0 < nq; i0 += a.parts * N, load(i0)) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int h = (i0 + n * a.parts) * HP + lane / U;
+                if (h < a.Hq) {
+                    if (turns) rope_unit(xa[n], xb[n], g, a.r.interleaved);
+                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + (t * a.Hq + h) * D;
+                    *reinterpret_cast<uint4*>(dst + ca) = xa[n];
+                    *reinterpret_cast<uint4*>(dst + cb) = xb[n];
+                }
+            }
         }
     }
     if (nt.page < 0) return;
     const int v = lane % LPH;                      // columns 8 v .. 8 v + 7
     const int row = nt.pos % kPageRows;
     // first pass of this part among the k and v passes nq .. nq + 2 nk
-    int i = part;
-    if (i < nq) i += (nq - i + a.parts - 1) / a.parts * a.parts;
-    for (; i < nq + 2 * nk; i += a.parts) {
-        const bool isk = i < nq + nk;
-        const int h = (isk ? i - nq : i - nq - nk) * HV + lane / LPH;
-        const bool live = h < a.Hkv;
-        const HeadRows& x = isk ? a.k : a.v;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = *reinterpret_cast<const uint4*>(x.p + t * x.row + h * x.head + 8 * v);
-        const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
-        float f[8];
+    int i0 = part;
+    if (i0 < nq) i0 += (nq - i0 + a.parts - 1) / a.parts * a.parts;
+    const int last = nq + 2 * nk;
+    uint4 raw[N];
+    auto load = [&](int from) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            f[2 * e] = bf16_lo(wd[e]);
-            f[2 * e + 1] = bf16_hi(wd[e]);
+        for (int n = 0; n < N; ++n) {
+            const int i = from + n * a.parts;
+            const bool isk = i < nq + nk;
+            const int h = (isk ? i - nq : i - nq - nk) * HV + lane / LPH;
+            const HeadRows& x = isk ? a.k : a.v;
+            raw[n] = make_uint4(0, 0, 0, 0);
+            if (i < last && h < a.Hkv) raw[n] = *reinterpret_cast<const uint4*>(x.p + t * x.row + h * x.head + 8 * v);
         }
-        if (isk && nrot) {
-            if (a.r.interleaved) {
-                if (v < 2 * nrot) {
-                    // pairs 4 v .. 4 v + 3: half of the eight whose angles start at 8 (v / 2)
-                    float c[8], s[8];
-                    rope_angles(a.r, t, a.total_new, v / 2, nt.pos, c, s);
+    };
+    load(i0);
+    // This lane's angles: of eight pairs (columns 8 v of one half), or of pairs 4 v .. 4 v + 3
+    // (interleaved: the first or second half of the eight from 8 (v / 2)).
+    const bool turns = v < 2 * nrot, first = v < nrot;
+    RopeAngles g;
+    if (turns && i0 < nq + nk)
+        g = rope_angles(a.r, t, a.total_new, a.r.interleaved ? v / 2 : first ? v : v - nrot, nt.pos);
+    for (; i0 < last; i0 += a.parts * N, load(i0)) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        rope_turn(f[2 * e], f[2 * e + 1], v & 1 ? c[4 + e] : c[e], v & 1 ? s[4 + e] : s[e]);
-                }
-            } else {
-                // columns 8 v .. of the first half turn with those 8 (v + nrot) .. of the second
-                const int mate = lane - v + (v < nrot ? v + nrot : v < 2 * nrot ? v - nrot : v);
-                uint32_t pw[4];
+        for (int n = 0; n < N; ++n) {
+            const int i = i0 + n * a.parts;
+            if (i >= last) break;
+            const bool isk = i < nq + nk;
+            const int h = (isk ? i - nq : i - nq - nk) * HV + lane / LPH;
+            const bool live = h < a.Hkv;
+            uint32_t wd[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+            if (isk && nrot) {
+                if (a.r.interleaved) {
+                    if (turns) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pw[e] = __shfl_sync(0xffffffffu, wd[e], mate);
-                if (v < 2 * nrot) {
-                    const bool first = v < nrot;
-                    float c[8], s[8];
-                    rope_angles(a.r, t, a.total_new, first ? v : v - nrot, nt.pos, c, s);
+                        for (int e = 0; e < 4; e += 2) {
+                            float2 x1 = make_float2(bf16_lo(wd[e]), bf16_lo(wd[e + 1]));
+                            float2 x2 = make_float2(bf16_hi(wd[e]), bf16_hi(wd[e + 1]));
+                            RopeAngles w;
+                            w.c[0] = v & 1 ? g.c[2 + e / 2] : g.c[e / 2];
+                            w.s[0] = v & 1 ? g.s[2 + e / 2] : g.s[e / 2];
+                            w.n[0] = v & 1 ? g.n[2 + e / 2] : g.n[e / 2];
+                            rope_turn(x1, x2, w, 0);
+                            wd[e] = pack_bf16(x1.x, x2.x);
+                            wd[e + 1] = pack_bf16(x1.y, x2.y);
+                        }
+                    }
+                } else {
+                    // columns 8 v .. of the first half turn with those 8 (v + nrot) .. of the second
+                    const int mate = lane - v + (!turns ? v : first ? v + nrot : v - nrot);
+                    uint32_t pw[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float m = e & 1 ? bf16_hi(pw[e / 2]) : bf16_lo(pw[e / 2]);
-                        float x1 = first ? f[e] : m, x2 = first ? m : f[e];
-                        rope_turn(x1, x2, c[e], s[e]);
-                        f[e] = first ? x1 : x2;
+                    for (int e = 0; e < 4; ++e) pw[e] = __shfl_sync(0xffffffffu, wd[e], mate);
+                    if (turns) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            // the first half's column: x1 c - x2 s; the second's: x2 c + x1 s
+                            const float2 y = fadd2(fmul2(bf16_pair(wd[e]), g.c[e]), fmul2(bf16_pair(pw[e]), first ? g.n[e] : g.s[e]));
+                            wd[e] = pack_bf16(y.x, y.y);
+                        }
                     }
                 }
             }
+            // the group's smallest and, negated, largest value side by side, across its lanes
+            const uint32_t lo2 = min_bf16x2(min_bf16x2(wd[0], wd[1]), min_bf16x2(wd[2], wd[3]));
+            const uint32_t hi2 = max_bf16x2(max_bf16x2(wd[0], wd[1]), max_bf16x2(wd[2], wd[3]));
+            uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2 ^ 0x80008000u, 0x5410), __byte_perm(lo2, hi2 ^ 0x80008000u, 0x7632));
+            ends = min_bf16x2(ends, 0u);           // (a group's range includes zero)
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                const uint32_t p = pack_bf16(f[e], f[e + 1]);
-                f[e] = bf16_lo(p);
-                f[e + 1] = bf16_hi(p);
-            }
-        }
-        float lo = 0.0f, hi = 0.0f;
+            for (int o = 1; o < GS / 8; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+            const Q4Group q = q4_group(bf16_lo(ends), -bf16_hi(ends));
+            const float2 f[4] = {bf16_pair(wd[0]), bf16_pair(wd[1]), bf16_pair(wd[2]), bf16_pair(wd[3])};
+            const uint32_t codes = q4_codes(f, q);
+            const long long tile = nt.page * a.Hkv + h;
+            if (isk) {
+                if (live) {
+                    uint32_t* kt = reinterpret_cast<uint32_t*>(a.k_cache + tile * (kPageRows * D / 2)) + row * (D / 8);
+                    kt[(v % 4) * W + v / 4] = codes;
+                }
+            } else {
+                // lane j of a quad holds nibble r of dims 32 u + 8 j + r; it takes pieces r = 2 j, 2 j + 1:
+                // byte j of the quad's four words
+                const int j = lane & 3;
+                uint32_t b[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            lo = min_nan(lo, f[e]);
-            hi = max_nan(hi, f[e]);
-        }
-#pragma unroll
-        for (int o = 1; o < GS / 8; o <<= 1) {
-            lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        }
-        const Q4Group g = q4_group(lo, hi);
-        uint32_t codes = q4_codes(f, g);
-        const long long tile = nt.page * a.Hkv + h;
-        if (isk) {
-            if (live) {
-                uint32_t* kt = reinterpret_cast<uint32_t*>(a.k_cache + tile * (kPageRows * D / 2)) + row * (D / 8);
-                kt[(v % 4) * W + v / 4] = codes;
+                for (int e = 0; e < 4; ++e) b[e] = __shfl_sync(0xffffffffu, codes, (lane & ~3) + e);
+                const uint32_t sel = j | (4 + j) << 4;
+                const uint32_t b01 = __byte_perm(b[0], b[1], sel), b23 = __byte_perm(b[2], b[3], sel);
+                const uint32_t all = __byte_perm(b01, b23, 0x5410);      // bytes of the four lanes
+                const uint32_t e4 = all & 0x0f0f0f0fu, o4 = (all >> 4) & 0x0f0f0f0fu;
+                const uint32_t even = (e4 | e4 >> 4) & 0x00ff00ffu, odd = (o4 | o4 >> 4) & 0x00ff00ffu;
+                if (live) {
+                    uint16_t* vt = reinterpret_cast<uint16_t*>(a.v_cache + tile * (kPageRows * D / 2));
+                    const int at = (((row / 8) * 8 * 4 + row % 8 / 2) * W + v / 4) * 2 + row % 2;   // piece r = 0
+                    vt[at + 2 * j * 4 * W * 2] = (uint16_t)(even | even >> 8);
+                    vt[at + (2 * j + 1) * 4 * W * 2] = (uint16_t)(odd | odd >> 8);
+                }
             }
-        } else {
-            // lane j of a quad holds nibble r of dims 32 u + 8 j + r; it takes pieces r = 2 j, 2 j + 1
-            const int j = lane & 3;
-            uint32_t q[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t other = __shfl_sync(0xffffffffu, codes, (lane & ~3) + e);
-                q[e] = (other >> (8 * j)) & 0xffu;
-            }
-            const uint32_t even = (q[0] & 15u) | (q[1] & 15u) << 4 | (q[2] & 15u) << 8 | (q[3] & 15u) << 12;
-            const uint32_t odd = q[0] >> 4 | (q[1] >> 4) << 4 | (q[2] >> 4) << 8 | (q[3] >> 4) << 12;
-            if (live) {
-                uint16_t* vt = reinterpret_cast<uint16_t*>(a.v_cache + tile * (kPageRows * D / 2));
-                const int at = (((row / 8) * 8 * 4 + row % 8 / 2) * W + v / 4) * 2 + row % 2;   // piece r = 0
-                vt[at + 2 * j * 4 * W * 2] = (uint16_t)even;
-                vt[at + (2 * j + 1) * 4 * W * 2] = (uint16_t)odd;
-            }
+            if (live && v % (GS / 8) == 0)
+                (isk ? a.k_meta : a.v_meta)[(tile * kPageRows + row) * G + v / (GS / 8)] = (uint16_t)q.meta;
         }
-        if (live && v % (GS / 8) == 0)
-            (isk ? a.k_meta : a.v_meta)[(tile * kPageRows + row) * G + v / (GS / 8)] = (uint16_t)g.meta;
     }
 }
 

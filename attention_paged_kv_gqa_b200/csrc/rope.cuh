@@ -22,7 +22,7 @@
 
 namespace attn {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxAxes = 4;
 // kErrRope*: a position outside the table, an axis outside the given ones.
 // kErrAppend* as in append.cuh.
@@ -39,9 +39,13 @@ struct RopeTable {
     float sign;              // -1: the inverse rotation (the gradient)
 };
 
-// Cosines and sines of the eight pairs 8 u .. 8 u + 7 of token t.
-__device__ __forceinline__ void rope_angles(const RopeTable& r, long long t, long long total, int u, int seq_pos,
-                                            float (&c)[8], float (&s)[8]) {
+// Cosines, sines and minus sines of the pairs 2 i and 2 i + 1 of eight, for packed arithmetic.
+struct RopeAngles {
+    float2 c[4], s[4], n[4];
+};
+
+// The eight pairs 8 u .. 8 u + 7 of token t.
+__device__ __forceinline__ RopeAngles rope_angles(const RopeTable& r, long long t, long long total, int u, int seq_pos) {
     const int half = r.rot / 2;
     auto place = [&](int axis) {
         int p = r.positions ? __ldg(r.positions + axis * total + t) : seq_pos;
@@ -51,7 +55,7 @@ __device__ __forceinline__ void rope_angles(const RopeTable& r, long long t, lon
         }
         return p;
     };
-    int ax[8];
+    int ax[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     bool one = true;
     if (r.pair_axis) {
 #pragma unroll
@@ -63,66 +67,66 @@ __device__ __forceinline__ void rope_angles(const RopeTable& r, long long t, lon
             }
             one = one && ax[i] == ax[0];
         }
-    } else {
-        ax[0] = 0;
     }
+    RopeAngles g;
     if (one) {
         const float* row = r.table + (long long)place(ax[0]) * r.rot + 8 * u;
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-            const float4 cv = __ldg(reinterpret_cast<const float4*>(row + i));
-            const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + i));
-            c[i] = cv.x, c[i + 1] = cv.y, c[i + 2] = cv.z, c[i + 3] = cv.w;
-            s[i] = sv.x, s[i + 1] = sv.y, s[i + 2] = sv.z, s[i + 3] = sv.w;
+        for (int i = 0; i < 4; i += 2) {
+            const float4 cv = __ldg(reinterpret_cast<const float4*>(row + 2 * i));
+            const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half + 2 * i));
+            g.c[i] = make_float2(cv.x, cv.y), g.c[i + 1] = make_float2(cv.z, cv.w);
+            g.s[i] = make_float2(sv.x, sv.y), g.s[i + 1] = make_float2(sv.z, sv.w);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float* row = r.table + (long long)place(ax[i]) * r.rot + 8 * u + i;
-            c[i] = __ldg(row);
-            s[i] = __ldg(row + half);
+        for (int i = 0; i < 4; ++i) {
+            const float* r0 = r.table + (long long)place(ax[2 * i]) * r.rot + 8 * u + 2 * i;
+            const float* r1 = r.table + (long long)place(ax[2 * i + 1]) * r.rot + 8 * u + 2 * i + 1;
+            g.c[i] = make_float2(__ldg(r0), __ldg(r1));
+            g.s[i] = make_float2(__ldg(r0 + half), __ldg(r1 + half));
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= r.sign;
+    for (int i = 0; i < 4; ++i) {
+        g.s[i] = make_float2(g.s[i].x * r.sign, g.s[i].y * r.sign);
+        g.n[i] = make_float2(-g.s[i].x, -g.s[i].y);
+    }
+    return g;
 }
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) { return make_float2(bf16_lo(w), bf16_hi(w)); }
 
-// Turns the pair (x1, x2); every operation rounded by itself.
-__device__ __forceinline__ void rope_turn(float& x1, float& x2, float c, float s) {
-    const float y1 = __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
-    x2 = __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+// Turns two pairs (x1, x2) by the angles 2 i and 2 i + 1: packed, every operation rounded by itself.
+__device__ __forceinline__ void rope_turn(float2& x1, float2& x2, const RopeAngles& g, int i) {
+    const float2 y1 = fadd2(fmul2(x1, g.c[i]), fmul2(x2, g.n[i]));
+    x2 = fadd2(fmul2(x2, g.c[i]), fmul2(x1, g.s[i]));
     x1 = y1;
 }
 
 // Turns a unit: pieces a and b hold the first and second columns of the eight
 // pairs, or eight interleaved pairs in order.
-__device__ __forceinline__ void rope_unit(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8], bool interleaved) {
-    uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
-    uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
-    if (interleaved) {
+__device__ __forceinline__ void rope_unit(uint4& a, uint4& b, const RopeAngles& g, bool interleaved) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x1 = bf16_lo(wa[i]), x2 = bf16_hi(wa[i]);
-            rope_turn(x1, x2, c[i], s[i]);
-            wa[i] = pack_bf16(x1, x2);
-            x1 = bf16_lo(wb[i]), x2 = bf16_hi(wb[i]);
-            rope_turn(x1, x2, c[4 + i], s[4 + i]);
-            wb[i] = pack_bf16(x1, x2);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float x1 = bf16_lo(wa[i]), x2 = bf16_lo(wb[i]);
-            float z1 = bf16_hi(wa[i]), z2 = bf16_hi(wb[i]);
-            rope_turn(x1, x2, c[2 * i], s[2 * i]);
-            rope_turn(z1, z2, c[2 * i + 1], s[2 * i + 1]);
-            wa[i] = pack_bf16(x1, z1);
-            wb[i] = pack_bf16(x2, z2);
+    for (int i = 0; i < 4; ++i) {
+        if (interleaved) {
+            float2 x1 = make_float2(bf16_lo(w[2 * i]), bf16_lo(w[2 * i + 1]));
+            float2 x2 = make_float2(bf16_hi(w[2 * i]), bf16_hi(w[2 * i + 1]));
+            rope_turn(x1, x2, g, i);
+            w[2 * i] = pack_bf16(x1.x, x2.x);
+            w[2 * i + 1] = pack_bf16(x1.y, x2.y);
+        } else {
+            float2 x1 = bf16_pair(w[i]), x2 = bf16_pair(w[4 + i]);
+            rope_turn(x1, x2, g, i);
+            w[i] = pack_bf16(x1.x, x1.y);
+            w[4 + i] = pack_bf16(x2.x, x2.y);
         }
     }
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // Columns of unit u's two pieces.  Units past rot / 16 hold the columns that do
@@ -163,37 +167,41 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     if (t >= a.total) return;
     const int u = lane % U;
     const bool turns = u < a.r.rot / 16;
-    float c[8], s[8];
-    if (turns) rope_angles(a.r, t, a.total, u, 0, c, s);
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
     const int H = a.Hq + a.Hkv;
     constexpr int N = 4;                 // head groups whose loads are in flight together
-    for (int h0 = part * HP + lane / U; h0 < H; h0 += a.parts * HP * N) {
-        uint4 xa[N], xb[N];
-        __nv_bfloat16* dst[N];
+    uint4 xa[N], xb[N];
+    auto load = [&](int h0) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int h = h0 + n * a.parts * HP;
             if (h < H) {
-                const bool isq = h < a.Hq;
-                const __nv_bfloat16* src = isq ? a.q.p + t * a.q.row + h * a.q.head
-                                               : a.k.p + t * a.k.row + (h - a.Hq) * a.k.head;
-                dst[n] = isq ? a.q_out + t * a.qo_row + h * a.qo_head
-                             : a.k_out + t * a.ko_row + (h - a.Hq) * a.ko_head;
+                const __nv_bfloat16* src = h < a.Hq ? a.q.p + t * a.q.row + h * a.q.head
+                                                    : a.k.p + t * a.k.row + (h - a.Hq) * a.k.head;
                 xa[n] = *reinterpret_cast<const uint4*>(src + ca);
                 xb[n] = *reinterpret_cast<const uint4*>(src + cb);
             }
         }
+    };
+    int h0 = part * HP + lane / U;
+    load(h0);                            // in flight while the angles are looked up
+    RopeAngles g;
+    if (turns) g = rope_angles(a.r, t, a.total, u, 0);
+    while (h0 < H) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int h = h0 + n * a.parts * HP;
             if (h < H) {
-                if (turns) rope_unit(xa[n], xb[n], c, s, a.r.interleaved);
-                *reinterpret_cast<uint4*>(dst[n] + ca) = xa[n];
-                *reinterpret_cast<uint4*>(dst[n] + cb) = xb[n];
+                if (turns) rope_unit(xa[n], xb[n], g, a.r.interleaved);
+                __nv_bfloat16* dst = h < a.Hq ? a.q_out + t * a.qo_row + h * a.qo_head
+                                              : a.k_out + t * a.ko_row + (h - a.Hq) * a.ko_head;
+                *reinterpret_cast<uint4*>(dst + ca) = xa[n];
+                *reinterpret_cast<uint4*>(dst + cb) = xb[n];
             }
         }
+        h0 += a.parts * HP * N;
+        load(h0);
     }
 }
 
@@ -221,34 +229,37 @@ struct NewToken {
     long long page;
 };
 
-__device__ __forceinline__ NewToken find_new_token(const RopeAppendArgs& a, int t, bool report) {
+__device__ __forceinline__ NewToken find_new_token(const RopeAppendArgs& a, int t, int lane) {
     NewToken n;
     int first = t;
     n.b = t;
     n.page = -1;
     n.pos = 0;
     if (a.cu_new) {
-        if (t < __ldg(&a.cu_new[0]) || t >= __ldg(&a.cu_new[a.B])) {
-            n.b = -1;
-            return n;
+        const int begin = __ldg(&a.cu_new[0]), end = __ldg(&a.cu_new[a.B]);
+        // the largest b with cu_new[b] <= t, 32 candidates at a time
+        int b = 0;
+        first = begin;
+        for (int len = a.B; len > 0;) {
+            const int step = (len + 31) / 32, i = lane * step;
+            const int c = i < len ? __ldg(&a.cu_new[b + i]) : 0;
+            const int k = max(__popc(__ballot_sync(0xffffffffu, i < len && c <= t)) - 1, 0);
+            first = __shfl_sync(0xffffffffu, c, k);
+            b += k * step;
+            len = step == 1 ? 0 : min(step, len - k * step);
         }
-        int lo = 0, hi = a.B;           // the largest b with cu_new[b] <= t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(&a.cu_new[mid]) <= t) lo = mid; else hi = mid;
-        }
-        n.b = lo;
-        first = __ldg(&a.cu_new[lo]);
+        n.b = t < begin || t >= end ? -1 : b;
+        if (n.b < 0) return n;
     }
     n.pos = __ldg(&a.seqused_k[n.b]) + (t - first);
     const int slot = n.pos >= 0 ? n.pos / kPageRows : -1;
     if (slot < 0 || slot >= a.max_blocks) {
-        if (report) record_data_error(kErrAppendSlot);
+        if (lane == 0) record_data_error(kErrAppendSlot);
         return n;
     }
     const int page = __ldg(&a.block_table[(long long)n.b * a.max_blocks + slot]);
     if (page < 0 || page >= a.num_blocks) {
-        if (report) record_data_error(kErrAppendPage);
+        if (lane == 0) record_data_error(kErrAppendPage);
         return n;
     }
     n.page = page;
@@ -260,9 +271,11 @@ __device__ __forceinline__ uint2 bf16x8_to_e4m3(uint4 x, float inv) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        o[i] = pack_e4m3x4(bf16_lo(w[2 * i]) * inv, bf16_hi(w[2 * i]) * inv, bf16_lo(w[2 * i + 1]) * inv,
-                           bf16_hi(w[2 * i + 1]) * inv);
+    for (int i = 0; i < 2; ++i) {
+        const float2 lo = fmul2(bf16_pair(w[2 * i]), make_float2(inv, inv));
+        const float2 hi = fmul2(bf16_pair(w[2 * i + 1]), make_float2(inv, inv));
+        o[i] = pack_e4m3x4(lo.x, lo.y, hi.x, hi.y);
+    }
     return make_uint2(o[0], o[1]);
 }
 
@@ -285,14 +298,31 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeApp
     const long long t = w / a.parts;
     const int part = (int)(w % a.parts);
     if (t >= a.total_new) return;
-    const NewToken nt = find_new_token(a, (int)t, lane == 0);
-    if (nt.b < 0) return;
     const int u = lane % U;
     const bool turns = a.r.table && u < a.r.rot / 16;
-    float c[8], s[8];
-    if (turns) rope_angles(a.r, t, a.total_new, u, nt.pos, c, s);
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
+    const int H = a.Hq + 2 * a.Hkv;
+    constexpr int N = 4;
+    uint4 xa[N], xb[N];
+    auto load = [&](int h0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int h = h0 + n * a.parts * HP;
+            if (h < H) {
+                const HeadRows& x = h < a.Hq ? a.q : h < a.Hq + a.Hkv ? a.k : a.v;
+                const __nv_bfloat16* src = x.p + t * x.row + (h < a.Hq ? h : h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv) * x.head;
+                xa[n] = *reinterpret_cast<const uint4*>(src + ca);
+                xb[n] = *reinterpret_cast<const uint4*>(src + cb);
+            }
+        }
+    };
+    int h0 = part * HP + lane / U;
+    load(h0);                            // in flight while the token's page and angles are looked up
+    const NewToken nt = find_new_token(a, (int)t, lane);
+    if (nt.b < 0) return;
+    RopeAngles g;
+    if (turns) g = rope_angles(a.r, t, a.total_new, u, nt.pos);
     float iq = 1.0f, ik = 1.0f, iv = 1.0f;
     if (CACHE == kCacheE4m3) {
         if (a.q.p) iq = __frcp_rn(__ldg(a.descale_q));
@@ -300,45 +330,27 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeApp
         iv = __frcp_rn(__ldg(a.descale_v));
     }
     const long long row0 = (nt.page * kPageRows + nt.pos % kPageRows) * a.Hkv;   // cache row of KV head 0
-    const int H = a.Hq + 2 * a.Hkv;
-    constexpr int N = 4;
-    for (int h0 = part * HP + lane / U; h0 < H; h0 += a.parts * HP * N) {
-        uint4 xa[N], xb[N];
-        uint8_t* dst[N];
+    while (h0 < H) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int h = h0 + n * a.parts * HP;
-            dst[n] = nullptr;
-            if (h >= H) continue;
-            const __nv_bfloat16* src;
-            if (h < a.Hq) {
-                src = a.q.p + t * a.q.row + h * a.q.head;
-                dst[n] = static_cast<uint8_t*>(a.q_out) + (t * a.Hq + h) * (D * E);
-            } else if (nt.page >= 0) {
-                const bool isk = h < a.Hq + a.Hkv;
-                const int g = h - a.Hq - (isk ? 0 : a.Hkv);
-                src = isk ? a.k.p + t * a.k.row + g * a.k.head : a.v.p + t * a.v.row + g * a.v.head;
-                dst[n] = (isk ? a.k_cache : a.v_cache) + (row0 + g) * (D * E);
-            } else {
-                continue;
-            }
-            xa[n] = *reinterpret_cast<const uint4*>(src + ca);
-            xb[n] = *reinterpret_cast<const uint4*>(src + cb);
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            if (!dst[n]) continue;
-            const int h = h0 + n * a.parts * HP;
-            if (turns && h < a.Hq + a.Hkv) rope_unit(xa[n], xb[n], c, s, a.r.interleaved);
+            const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
+            if (h >= H || (!isq && nt.page < 0)) continue;
+            uint8_t* dst = isq   ? static_cast<uint8_t*>(a.q_out) + (t * a.Hq + h) * (D * E)
+                           : isk ? a.k_cache + (row0 + h - a.Hq) * (D * E)
+                                 : a.v_cache + (row0 + h - a.Hq - a.Hkv) * (D * E);
+            if (turns && (isq || isk)) rope_unit(xa[n], xb[n], g, a.r.interleaved);
             if (CACHE == kCacheE4m3) {
-                const float inv = h < a.Hq ? iq : h < a.Hq + a.Hkv ? ik : iv;
-                *reinterpret_cast<uint2*>(dst[n] + ca) = bf16x8_to_e4m3(xa[n], inv);
-                *reinterpret_cast<uint2*>(dst[n] + cb) = bf16x8_to_e4m3(xb[n], inv);
+                const float inv = isq ? iq : isk ? ik : iv;
+                *reinterpret_cast<uint2*>(dst + ca) = bf16x8_to_e4m3(xa[n], inv);
+                *reinterpret_cast<uint2*>(dst + cb) = bf16x8_to_e4m3(xb[n], inv);
             } else {
-                *reinterpret_cast<uint4*>(dst[n] + 2 * ca) = xa[n];
-                *reinterpret_cast<uint4*>(dst[n] + 2 * cb) = xb[n];
+                *reinterpret_cast<uint4*>(dst + 2 * ca) = xa[n];
+                *reinterpret_cast<uint4*>(dst + 2 * cb) = xb[n];
             }
         }
+        h0 += a.parts * HP * N;
+        load(h0);
     }
 }
 

@@ -486,8 +486,8 @@ attn_status_t attn_rope(
  *                in the cache.
  *   descale_*    e4m3: device fp32 scalars, descale_q only with q.
  *   others       as in attn_kv_append_paged.  Rows of q, k_new and v_new outside
- *                [cu_seqlens_new[0], cu_seqlens_new[B]) are not read and theirs of
- *                q_out not written.
+ *                [cu_seqlens_new[0], cu_seqlens_new[B]) have no effect: theirs of
+ *                q_out are not written.
  * A token whose page or position is out of range is not written to the cache
  * (codes 501, 502); its row of q_out is.  Supported: head_dim in {64, 128}.
  */
