@@ -20,6 +20,8 @@
 // bank conflicts and without a transposition.
 #pragma once
 
+#include <type_traits>
+
 #include "append.cuh"
 #include "decode.cuh"
 #include "rope.cuh"
@@ -56,17 +58,20 @@ __device__ __forceinline__ float q4_nearest(float x, float inv) {
     return __fadd_rn(__fmaf_rn(x, inv, 768.0f), kQ4Magic - 768.0f);
 }
 
-// Step and zero of a group from its lo <= 0 and hi >= 0 (NaN where it has one).
+// Step and zero of a group from its lo <= 0 and hi >= 0 (NaN where it has one).  width / 15
+// up to 4 significant bits without a division: a candidate from a product that is a little
+// low, and one notch more where 15 of them still fall short.
 __device__ __forceinline__ Q4Group q4_group(float lo, float hi) {
     Q4Group g;
-    const float s = __fdiv_rn(__fsub_rn(hi, lo), 15.0f);
+    const float width = __fsub_rn(hi, lo);
+    const float s = __fmul_rn(width, 0.06666663f);   // 1 / 15 less 2^-21 of it
     uint32_t bits = (__float_as_uint(s) + 0xfffffu) & 0xfff00000u;
-    if (!(s < INFINITY)) bits = 0x7fc00000u;         // NaN or an infinity in the group
-    else if (__uint_as_float(bits) < 7.888609052210118e-31f) bits = 0;   // 2^-100
-    const bool live = bits != 0 && bits != 0x7fc00000u;
-    g.inv = live ? __frcp_rn(__uint_as_float(bits)) : 0.0f;
-    g.zero = live ? __fsub_rn(q4_nearest(-lo, g.inv), kQ4Magic) : 0.0f;
-    g.meta = (bits >> 16) | (uint32_t)(int)g.zero;
+    if (__fmaf_rn(-15.0f, __uint_as_float(bits), width) > 0.0f) bits += 0x100000u;
+    const bool live = bits >= 0x0d800000u && width < INFINITY;       // 2^-100; a NaN is not less
+    g.inv = live ? rcp_approx(__uint_as_float(bits)) : 0.0f;         // (see q4_nearest)
+    const float z = live ? q4_nearest(-lo, g.inv) : kQ4Magic;
+    g.zero = __fsub_rn(z, kQ4Magic);
+    g.meta = live ? (bits >> 16) | (__float_as_uint(z) & 15u) : width < INFINITY ? 0u : 0x7fc0u;
     return g;
 }
 
@@ -115,151 +120,131 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q4_kernel(const Rope
     const int part = (int)(w % a.parts);
     if (t >= a.total_new) return;
     const int nrot = a.r.table ? a.r.rot / 16 : 0;
-    const int nq = (a.Hq + HP - 1) / HP, nk = (a.Hkv + HV - 1) / HV;   // passes over q; over k, over v
-    constexpr int N = 4;                           // passes whose loads are in flight together
-
     NewToken nt;
     {
-        const int u = lane % U;
+        const int u = lane % U, first = part * HP + lane / U;
         const bool turns = u < nrot;
         int ca, cb;
         rope_columns(a.r, u, &ca, &cb);
-        uint4 xa[N], xb[N];
-        auto load = [&](int i0) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int h = (i0 + n * a.parts) * HP + lane / U;
-                if (h < a.Hq) {
-                    const __nv_bfloat16* src = a.q.p + t * a.q.row + h * a.q.head;
-                    xa[n] = *reinterpret_cast<const uint4*>(src + ca);
-                    xb[n] = *reinterpret_cast<const uint4*>(src + cb);
-                }
-            }
-        };
-        load(part);                                // in flight while the page and the angles are looked up
+        RopeRows<D> q;
+        q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the page and the angles are looked up
         nt = find_new_token(a, (int)t, lane);
         if (nt.b < 0) return;
         RopeAngles g;
-        if (turns && part < nq) g = rope_angles(a.r, t, a.total_new, u, nt.pos);
-        for (int i0 = part; i0 < nq; i0 += a.parts * N, load(i0)) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int h = (i0 + n * a.parts) * HP + lane / U;
-                if (h < a.Hq) {
-                    if (turns) rope_unit(xa[n], xb[n], g, a.r.interleaved);
-                    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.q_out) + (t * a.Hq + h) * D;
-                    *reinterpret_cast<uint4*>(dst + ca) = xa[n];
-                    *reinterpret_cast<uint4*>(dst + cb) = xb[n];
-                }
-            }
-        }
+        if (turns && a.q.p) g = rope_angles(a.r, t, a.total_new, u, nt.pos);
+        q.template finish<kCacheBf16>(static_cast<uint8_t*>(a.q_out) + ((t * a.Hq + first) * D + ca) * 2,
+                                      2LL * a.parts * HP * D, turns, g, a.r.interleaved, 1.0f);
     }
     if (nt.page < 0) return;
     const int v = lane % LPH;                      // columns 8 v .. 8 v + 7
     const int row = nt.pos % kPageRows;
-    // first pass of this part among the k and v passes nq .. nq + 2 nk
-    int i0 = part;
-    if (i0 < nq) i0 += (nq - i0 + a.parts - 1) / a.parts * a.parts;
-    const int last = nq + 2 * nk;
-    uint4 raw[N];
-    auto load = [&](int from) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int i = from + n * a.parts;
-            const bool isk = i < nq + nk;
-            const int h = (isk ? i - nq : i - nq - nk) * HV + lane / LPH;
-            const HeadRows& x = isk ? a.k : a.v;
-            raw[n] = make_uint4(0, 0, 0, 0);
-            if (i < last && h < a.Hkv) raw[n] = *reinterpret_cast<const uint4*>(x.p + t * x.row + h * x.head + 8 * v);
-        }
-    };
-    load(i0);
     // This lane's angles: of eight pairs (columns 8 v of one half), or of pairs 4 v .. 4 v + 3
     // (interleaved: the first or second half of the eight from 8 (v / 2)).
-    const bool turns = v < 2 * nrot, first = v < nrot;
+    const bool turns = v < 2 * nrot, front = v < nrot;
     RopeAngles g;
-    if (turns && i0 < nq + nk)
-        g = rope_angles(a.r, t, a.total_new, a.r.interleaved ? v / 2 : first ? v : v - nrot, nt.pos);
-    for (; i0 < last; i0 += a.parts * N, load(i0)) {
+    if (turns) {
+        g = rope_angles(a.r, t, a.total_new, a.r.interleaved ? v / 2 : front ? v : v - nrot, nt.pos);
+        if (a.r.interleaved && (v & 1)) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int i = i0 + n * a.parts;
-            if (i >= last) break;
-            const bool isk = i < nq + nk;
-            const int h = (isk ? i - nq : i - nq - nk) * HV + lane / LPH;
-            const bool live = h < a.Hkv;
-            uint32_t wd[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
-            if (isk && nrot) {
-                if (a.r.interleaved) {
-                    if (turns) {
+            for (int e = 0; e < 2; ++e) g.c[e] = g.c[2 + e], g.s[e] = g.s[2 + e], g.n[e] = g.n[2 + e];
+        }
+        if (!a.r.interleaved && front) {           // the first half's column: x1 c - x2 s; the second's: x2 c + x1 s
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            float2 x1 = make_float2(bf16_lo(wd[e]), bf16_lo(wd[e + 1]));
-                            float2 x2 = make_float2(bf16_hi(wd[e]), bf16_hi(wd[e + 1]));
-                            RopeAngles w;
-                            w.c[0] = v & 1 ? g.c[2 + e / 2] : g.c[e / 2];
-                            w.s[0] = v & 1 ? g.s[2 + e / 2] : g.s[e / 2];
-                            w.n[0] = v & 1 ? g.n[2 + e / 2] : g.n[e / 2];
-                            rope_turn(x1, x2, w, 0);
-                            wd[e] = pack_bf16(x1.x, x2.x);
-                            wd[e + 1] = pack_bf16(x1.y, x2.y);
-                        }
-                    }
-                } else {
-                    // columns 8 v .. of the first half turn with those 8 (v + nrot) .. of the second
-                    const int mate = lane - v + (!turns ? v : first ? v + nrot : v - nrot);
-                    uint32_t pw[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) pw[e] = __shfl_sync(0xffffffffu, wd[e], mate);
-                    if (turns) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // the first half's column: x1 c - x2 s; the second's: x2 c + x1 s
-                            const float2 y = fadd2(fmul2(bf16_pair(wd[e]), g.c[e]), fmul2(bf16_pair(pw[e]), first ? g.n[e] : g.s[e]));
-                            wd[e] = pack_bf16(y.x, y.y);
-                        }
-                    }
-                }
-            }
-            // the group's smallest and, negated, largest value side by side, across its lanes
-            const uint32_t lo2 = min_bf16x2(min_bf16x2(wd[0], wd[1]), min_bf16x2(wd[2], wd[3]));
-            const uint32_t hi2 = max_bf16x2(max_bf16x2(wd[0], wd[1]), max_bf16x2(wd[2], wd[3]));
-            uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2 ^ 0x80008000u, 0x5410), __byte_perm(lo2, hi2 ^ 0x80008000u, 0x7632));
-            ends = min_bf16x2(ends, 0u);           // (a group's range includes zero)
-#pragma unroll
-            for (int o = 1; o < GS / 8; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
-            const Q4Group q = q4_group(bf16_lo(ends), -bf16_hi(ends));
-            const float2 f[4] = {bf16_pair(wd[0]), bf16_pair(wd[1]), bf16_pair(wd[2]), bf16_pair(wd[3])};
-            const uint32_t codes = q4_codes(f, q);
-            const long long tile = nt.page * a.Hkv + h;
-            if (isk) {
-                if (live) {
-                    uint32_t* kt = reinterpret_cast<uint32_t*>(a.k_cache + tile * (kPageRows * D / 2)) + row * (D / 8);
-                    kt[(v % 4) * W + v / 4] = codes;
-                }
-            } else {
-                // lane j of a quad holds nibble r of dims 32 u + 8 j + r; it takes pieces r = 2 j, 2 j + 1:
-                // byte j of the quad's four words
-                const int j = lane & 3;
-                uint32_t b[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) b[e] = __shfl_sync(0xffffffffu, codes, (lane & ~3) + e);
-                const uint32_t sel = j | (4 + j) << 4;
-                const uint32_t b01 = __byte_perm(b[0], b[1], sel), b23 = __byte_perm(b[2], b[3], sel);
-                const uint32_t all = __byte_perm(b01, b23, 0x5410);      // bytes of the four lanes
-                const uint32_t e4 = all & 0x0f0f0f0fu, o4 = (all >> 4) & 0x0f0f0f0fu;
-                const uint32_t even = (e4 | e4 >> 4) & 0x00ff00ffu, odd = (o4 | o4 >> 4) & 0x00ff00ffu;
-                if (live) {
-                    uint16_t* vt = reinterpret_cast<uint16_t*>(a.v_cache + tile * (kPageRows * D / 2));
-                    const int at = (((row / 8) * 8 * 4 + row % 8 / 2) * W + v / 4) * 2 + row % 2;   // piece r = 0
-                    vt[at + 2 * j * 4 * W * 2] = (uint16_t)(even | even >> 8);
-                    vt[at + (2 * j + 1) * 4 * W * 2] = (uint16_t)(odd | odd >> 8);
-                }
-            }
-            if (live && v % (GS / 8) == 0)
-                (isk ? a.k_meta : a.v_meta)[(tile * kPageRows + row) * G + v / (GS / 8)] = (uint16_t)q.meta;
+            for (int e = 0; e < 4; ++e) g.s[e] = g.n[e];
         }
     }
+    constexpr int N = 4;                           // passes whose loads are in flight together
+    auto rows = [&](const HeadRows& x, uint8_t* cache, uint16_t* metas, auto is_k) {
+        constexpr bool K = decltype(is_k)::value;
+        int h = part * HV + lane / LPH;
+        const int apart = a.parts * HV;
+        const __nv_bfloat16* src = x.p + t * x.row + h * x.head + 8 * v;
+        const long long pitch = apart * x.head;
+        const long long tile0 = nt.page * a.Hkv;
+        // the lane's word of a K row, or its pieces r = 2 j and 2 j + 1 of a V tile
+        uint8_t* code = cache + (tile0 + h) * (kPageRows * D / 2) +
+                        (K ? row * (D / 2) + ((v % 4) * W + v / 4) * 4
+                           : ((((row / 8) * 8 + 2 * (lane & 3)) * 4 + row % 8 / 2) * W + v / 4) * 4 + row % 2 * 2);
+        uint16_t* meta = metas + ((tile0 + h) * kPageRows + row) * G + v / (GS / 8);
+        // (the number of passes is the warp's, so that all lanes shuffle)
+        for (int h0 = part * HV; h0 < a.Hkv; h0 += N * apart) {
+            uint4 raw[N];
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                raw[n] = make_uint4(0, 0, 0, 0);
+                if (h + n * apart < a.Hkv) raw[n] = *reinterpret_cast<const uint4*>(src + n * pitch);
+            }
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if (h0 + n * apart >= a.Hkv) break;
+                const bool live = h + n * apart < a.Hkv;
+                uint32_t wd[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+                if (K && nrot) {
+                    if (a.r.interleaved) {
+                        if (turns) {
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                float2 x1 = make_float2(bf16_lo(wd[e]), bf16_lo(wd[e + 1]));
+                                float2 x2 = make_float2(bf16_hi(wd[e]), bf16_hi(wd[e + 1]));
+                                rope_turn(x1, x2, g, e / 2);
+                                wd[e] = pack_bf16(x1.x, x2.x);
+                                wd[e + 1] = pack_bf16(x1.y, x2.y);
+                            }
+                        }
+                    } else {
+                        // columns 8 v .. of the first half turn with those 8 (v + nrot) .. of the second
+                        const int mate = lane + (!turns ? 0 : front ? nrot : -nrot);
+                        uint32_t pw[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) pw[e] = __shfl_sync(0xffffffffu, wd[e], mate);
+                        if (turns) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float2 y = fadd2(fmul2(bf16_pair(wd[e]), g.c[e]), fmul2(bf16_pair(pw[e]), g.s[e]));
+                                wd[e] = pack_bf16(y.x, y.y);
+                            }
+                        }
+                    }
+                }
+                // the group's smallest and, negated, largest value side by side, across its lanes
+                const uint32_t lo2 = min_bf16x2(min_bf16x2(wd[0], wd[1]), min_bf16x2(wd[2], wd[3]));
+                const uint32_t hi2 = max_bf16x2(max_bf16x2(wd[0], wd[1]), max_bf16x2(wd[2], wd[3])) ^ 0x80008000u;
+                uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
+                ends = min_bf16x2(ends, 0u);           // (a group's range includes zero)
+#pragma unroll
+                for (int o = 1; o < GS / 8; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+                const Q4Group q = q4_group(bf16_lo(ends), -bf16_hi(ends));
+                const float2 f[4] = {bf16_pair(wd[0]), bf16_pair(wd[1]), bf16_pair(wd[2]), bf16_pair(wd[3])};
+                const uint32_t codes = q4_codes(f, q);
+                uint8_t* to = code + (long long)n * apart * (kPageRows * D / 2);
+                if (K) {
+                    if (live) *reinterpret_cast<uint32_t*>(to) = codes;
+                } else {
+                    // lane j of a quad holds nibble r of dims 32 u + 8 j + r; it takes byte j of the
+                    // quad's four words
+                    const int j = lane & 3;
+                    uint32_t b[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) b[e] = __shfl_sync(0xffffffffu, codes, (lane & ~3) + e);
+                    const uint32_t sel = j | (4 + j) << 4;
+                    const uint32_t all = __byte_perm(__byte_perm(b[0], b[1], sel), __byte_perm(b[2], b[3], sel), 0x5410);
+                    const uint32_t e4 = all & 0x0f0f0f0fu, o4 = (all >> 4) & 0x0f0f0f0fu;
+                    const uint32_t even = (e4 | e4 >> 4) & 0x00ff00ffu, odd = (o4 | o4 >> 4) & 0x00ff00ffu;
+                    if (live) {
+                        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(even | even >> 8);
+                        *reinterpret_cast<uint16_t*>(to + 16 * W) = (uint16_t)(odd | odd >> 8);
+                    }
+                }
+                if (live && v % (GS / 8) == 0) meta[(long long)n * apart * (kPageRows * G)] = (uint16_t)q.meta;
+            }
+            h += N * apart;
+            src += N * pitch;
+            code += (long long)N * apart * (kPageRows * D / 2);
+            meta += (long long)N * apart * (kPageRows * G);
+        }
+    };
+    rows(a.k, a.k_cache, a.k_meta, std::true_type());
+    rows(a.v, a.v_cache, a.v_meta, std::false_type());
 }
 
 // ---------------------------------------------------------------- read back
@@ -276,10 +261,43 @@ struct Q4GatherArgs {
     __nv_bfloat16 *k_out, *v_out;   // [total][Hkv][D]
 };
 
-// Two codes (nibbles at bits 0 and 16 of w) as step * (code - zero) in bf16x2.
-__device__ __forceinline__ uint32_t q4_pair(uint32_t w, float step, float zero) {
-    return pack_bf16(((float)(w & 15u) - zero) * step, ((float)((w >> 16) & 15u) - zero) * step);
+// N consecutive words (N = 2 or 4, aligned).
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
+    }
 }
+
+// The N metas (1, 2 or 4) of a token.
+template <int N>
+__device__ __forceinline__ void load_metas(const uint8_t* p, uint32_t (&m)[N]) {
+    if constexpr (N == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        m[0] = x.x & 0xffffu, m[1] = x.x >> 16, m[2] = x.y & 0xffffu, m[3] = x.y >> 16;
+    } else if constexpr (N == 2) {
+        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
+        m[0] = x & 0xffffu, m[1] = x >> 16;
+    } else {
+        m[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+}
+
+// The codes at the low nibbles of w's halves as step * (code - zero) in bf16: 128 + code has
+// 8 bits, its difference with 128 + zero is exact, and so is the product.
+__device__ __forceinline__ uint32_t q4_pair(uint32_t w, uint32_t step2, uint32_t zero2) {
+    uint32_t r = (w & 0x000f000fu) | 0x43004300u;
+    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(zero2));
+    asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(r) : "r"(step2));
+    return r;
+}
+// Steps, and 128 + zeros, of two metas (low and high half) in bf16.
+__device__ __forceinline__ uint32_t q4_steps(uint32_t m2) { return m2 & 0xfff0fff0u; }
+__device__ __forceinline__ uint32_t q4_zeros(uint32_t m2) { return (m2 & 0x000f000fu) | 0x43004300u; }
 
 // The rows of packed K and V from 4-bit pages: a warp takes the K and V tile of
 // one page and head.  The values are bf16 numbers, so nothing is lost.
@@ -355,55 +373,53 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
         };
         const uint16_t* km = a.k_meta + tile * kPageRows * G;
         const uint16_t* vm = a.v_meta + tile * kPageRows * G;
-        // K: 4 units (16-byte piece c) of W words in each of the 16 rows
+        // K: 4 units (16-byte piece c) of W words in each of the 16 rows; V: lane (token pair
+        // p = 4 a + c, word u) takes the eight words r = 0 .. 7 that hold its two tokens' dims
+        // 32 u + 8 j + r.  All of it is loaded first.
         const uint32_t* kt = reinterpret_cast<const uint32_t*>(a.k_cache + tile * (kPageRows * D / 2));
+        const uint32_t* vt = reinterpret_cast<const uint32_t*>(a.v_cache + tile * (kPageRows * D / 2));
+        const int u = lane % W, p = lane / W % 8;
+        uint32_t kw[2][W], kmeta[2][G], wr[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            load_words<W>(reinterpret_cast<const uint8_t*>(kt + (lane + 32 * i) * W), kw[i]);
+            load_metas<G>(reinterpret_cast<const uint8_t*>(km + (lane + 32 * i) / 4 * G), kmeta[i]);
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) wr[r] = __ldg(vt + (((p / 4) * 8 + r) * 4 + p % 4) * W + u);
+        const uint32_t vmeta = __ldg(vm + 2 * p * G + 32 * u / GS) | (uint32_t)__ldg(vm + (2 * p + 1) * G + 32 * u / GS) << 16;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int y = (lane + 32 * i) / 4, c = lane % 4;
             const long long r = out_row(y);
             if (r < 0) continue;
-            __nv_bfloat16* dst = a.k_out + (r * a.Hkv + h) * D;
+            __nv_bfloat16* dst = a.k_out + (r * a.Hkv + h) * D + 8 * c;
 #pragma unroll
-            for (int wi = 0; wi < W; ++wi) {
-                const uint32_t w = __ldg(kt + (y * 4 + c) * W + wi);
-                const uint32_t m = __ldg(km + y * G + 32 * wi / GS);
-                const float st = q4_step(m), z = q4_zero(m);
-                // nibble e at bits 4 e: pairs (0, 1), (2, 3) ...
-                uint32_t o[4];
+            for (int w = 0; w < W; ++w) {
+                const uint32_t m2 = kmeta[i][32 * w / GS] * 0x10001u, st = q4_steps(m2), z = q4_zeros(m2);
+                uint32_t x[4];                     // dims e and e + 4
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t p = w >> (8 * e);
-                    o[e] = q4_pair((p & 15u) | (p & 0xf0u) << 12, st, z);
-                }
-                *reinterpret_cast<uint4*>(dst + 32 * wi + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int e = 0; e < 4; ++e) x[e] = q4_pair(kw[i][w] >> (4 * e), st, z);
+                *reinterpret_cast<uint4*>(dst + 32 * w) =
+                    make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                               __byte_perm(x[2], x[3], 0x7632));
             }
         }
-        // V: lane (token pair p = 4 a + c, word u): the eight words r = 0 .. 7 hold its two
-        // tokens' dims 32 u + 8 j + r
-        const uint32_t* vt = reinterpret_cast<const uint32_t*>(a.v_cache + tile * (kPageRows * D / 2));
-        const int u = lane % W, p = lane / W;
-        if (p < 8) {
-            const int y = 2 * p;
-            uint32_t wr[8];
+        const long long r0 = lane / W < 8 ? out_row(2 * p) : -1, r1 = lane / W < 8 ? out_row(2 * p + 1) : -1;
+        const uint32_t st = q4_steps(vmeta), z = q4_zeros(vmeta);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) wr[r] = __ldg(vt + (((p / 4) * 8 + r) * 4 + p % 4) * W + u);
+        for (int j = 0; j < 4; ++j) {
+            uint32_t x[8];                         // dim 8 j + r of both tokens
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const long long r = out_row(y + half);
-                if (r < 0) continue;
-                const uint32_t m = __ldg(vm + (y + half) * G + 32 * u / GS);
-                const float st = q4_step(m), z = q4_zero(m);
-                __nv_bfloat16* dst = a.v_out + (r * a.Hkv + h) * D + 32 * u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int sh = 16 * half + 4 * j;
-                    uint32_t o[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[e] = q4_pair(((wr[2 * e] >> sh) & 15u) | ((wr[2 * e + 1] >> sh) & 15u) << 16, st, z);
-                    *reinterpret_cast<uint4*>(dst + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
+            for (int r = 0; r < 8; ++r) x[r] = q4_pair(wr[r] >> (4 * j), st, z);
+            if (r0 >= 0)
+                *reinterpret_cast<uint4*>(a.v_out + (r0 * a.Hkv + h) * D + 32 * u + 8 * j) =
+                    make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[4], x[5], 0x5410),
+                               __byte_perm(x[6], x[7], 0x5410));
+            if (r1 >= 0)
+                *reinterpret_cast<uint4*>(a.v_out + (r1 * a.Hkv + h) * D + 32 * u + 8 * j) =
+                    make_uint4(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632), __byte_perm(x[4], x[5], 0x7632),
+                               __byte_perm(x[6], x[7], 0x7632));
         }
     }
 }
@@ -515,32 +531,6 @@ __device__ __forceinline__ void q4_mma2(float2 (&d)[2], const uint32_t (&a)[4], 
         "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0].x), "+f"(d[0].y), "+f"(d[1].x), "+f"(d[1].y)
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// N consecutive words (N = 2 or 4, aligned) of shared memory.
-template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-    if constexpr (N == 4) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
-    }
-}
-
-// The N metas (1, 2 or 4) of a token.
-template <int N>
-__device__ __forceinline__ void load_metas(const uint8_t* p, uint32_t (&m)[N]) {
-    if constexpr (N == 4) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        m[0] = x.x & 0xffffu, m[1] = x.x >> 16, m[2] = x.y & 0xffffu, m[3] = x.y >> 16;
-    } else if constexpr (N == 2) {
-        const uint32_t x = *reinterpret_cast<const uint32_t*>(p);
-        m[0] = x & 0xffffu, m[1] = x >> 16;
-    } else {
-        m[0] = *reinterpret_cast<const uint16_t*>(p);
-    }
 }
 
 // Keys the sequence's queries can see start here (the window of its first query).

@@ -147,6 +147,75 @@ struct HeadRows {            // [token][head][D] with element strides
     long long row, head;
 };
 
+// Eight bf16 values times `inv`, as e4m3 (nearest even, saturating at +-448).
+__device__ __forceinline__ uint2 bf16x8_to_e4m3(uint4 x, float inv) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t o[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 lo = fmul2(bf16_pair(w[2 * i]), make_float2(inv, inv));
+        const float2 hi = fmul2(bf16_pair(w[2 * i + 1]), make_float2(inv, inv));
+        o[i] = pack_e4m3x4(lo.x, lo.y, hi.x, hi.y);
+    }
+    return make_uint2(o[0], o[1]);
+}
+
+// One token's rows of H heads (q, k or v) on their way: a warp takes every parts-th group of
+// HP heads, a lane its unit (pieces at columns ca and cb) of each.  N groups' loads are in
+// flight together; start() issues the first ones, before the caller looks the token up.
+template <int D>
+struct RopeRows {
+    static constexpr int U = D / 16, HP = 32 / U, N = 4;
+    const __nv_bfloat16* src;            // this lane's first group, piece a
+    long long pitch;                     // elements to its next group
+    int left, apart;                     // heads from its first one on, heads between its groups
+    int cb_ca;                           // piece b behind piece a
+    uint4 xa[N], xb[N];
+
+    __device__ __forceinline__ void load() {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n * apart < left) {
+                xa[n] = *reinterpret_cast<const uint4*>(src + n * pitch);
+                xb[n] = *reinterpret_cast<const uint4*>(src + n * pitch + cb_ca);
+            }
+    }
+    __device__ __forceinline__ void start(const HeadRows& x, long long t, int H, int first, int parts, int ca, int cb) {
+        src = x.p + t * x.row + first * x.head + ca;
+        pitch = parts * HP * x.head;
+        left = H - first;
+        apart = parts * HP;
+        cb_ca = cb - ca;
+        load();
+    }
+    // Writes them to dst (this lane's first group, piece a; `step` bytes to its next one) as bf16, or
+    // as e4m3 times inv; turned where `turns`.
+    template <int CACHE>
+    __device__ __forceinline__ void finish(uint8_t* dst, long long step, bool turns, const RopeAngles& g, bool interleaved,
+                                           float inv) {
+        constexpr int E = CACHE == kCacheE4m3 ? 1 : 2;
+        while (left > 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                if (n * apart < left) {
+                    if (turns) rope_unit(xa[n], xb[n], g, interleaved);
+                    uint8_t* to = dst + n * step;
+                    if (CACHE == kCacheE4m3) {
+                        *reinterpret_cast<uint2*>(to) = bf16x8_to_e4m3(xa[n], inv);
+                        *reinterpret_cast<uint2*>(to + cb_ca) = bf16x8_to_e4m3(xb[n], inv);
+                    } else {
+                        *reinterpret_cast<uint4*>(to) = xa[n];
+                        *reinterpret_cast<uint4*>(to + E * cb_ca) = xb[n];
+                    }
+                }
+            src += N * pitch;
+            dst += N * step;
+            left -= N * apart;
+            load();
+        }
+    }
+};
+
 struct RopeArgs {
     HeadRows q, k;           // k.p null: q alone
     __nv_bfloat16 *q_out, *k_out;
@@ -169,40 +238,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     const bool turns = u < a.r.rot / 16;
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
-    const int H = a.Hq + a.Hkv;
-    constexpr int N = 4;                 // head groups whose loads are in flight together
-    uint4 xa[N], xb[N];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int h = h0 + n * a.parts * HP;
-            if (h < H) {
-                const __nv_bfloat16* src = h < a.Hq ? a.q.p + t * a.q.row + h * a.q.head
-                                                    : a.k.p + t * a.k.row + (h - a.Hq) * a.k.head;
-                xa[n] = *reinterpret_cast<const uint4*>(src + ca);
-                xb[n] = *reinterpret_cast<const uint4*>(src + cb);
-            }
-        }
-    };
-    int h0 = part * HP + lane / U;
-    load(h0);                            // in flight while the angles are looked up
+    const int first = part * HP + lane / U;
+    RopeRows<D> q, k;
+    q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the angles are looked up
+    k.start(a.k, t, a.Hkv, first, a.parts, ca, cb);
     RopeAngles g;
     if (turns) g = rope_angles(a.r, t, a.total, u, 0);
-    while (h0 < H) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int h = h0 + n * a.parts * HP;
-            if (h < H) {
-                if (turns) rope_unit(xa[n], xb[n], g, a.r.interleaved);
-                __nv_bfloat16* dst = h < a.Hq ? a.q_out + t * a.qo_row + h * a.qo_head
-                                              : a.k_out + t * a.ko_row + (h - a.Hq) * a.ko_head;
-                *reinterpret_cast<uint4*>(dst + ca) = xa[n];
-                *reinterpret_cast<uint4*>(dst + cb) = xb[n];
-            }
-        }
-        h0 += a.parts * HP * N;
-        load(h0);
-    }
+    q.template finish<kCacheBf16>(reinterpret_cast<uint8_t*>(a.q_out + t * a.qo_row + first * a.qo_head + ca),
+                                  2 * a.parts * HP * a.qo_head, turns, g, a.r.interleaved, 1.0f);
+    k.template finish<kCacheBf16>(reinterpret_cast<uint8_t*>(a.k_out + t * a.ko_row + first * a.ko_head + ca),
+                                  2 * a.parts * HP * a.ko_head, turns, g, a.r.interleaved, 1.0f);
 }
 
 // ---------------------------------------------------------------- append
@@ -266,19 +311,6 @@ __device__ __forceinline__ NewToken find_new_token(const RopeAppendArgs& a, int 
     return n;
 }
 
-// Eight bf16 values times `inv`, as e4m3 (nearest even, saturating at +-448).
-__device__ __forceinline__ uint2 bf16x8_to_e4m3(uint4 x, float inv) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float2 lo = fmul2(bf16_pair(w[2 * i]), make_float2(inv, inv));
-        const float2 hi = fmul2(bf16_pair(w[2 * i + 1]), make_float2(inv, inv));
-        o[i] = pack_e4m3x4(lo.x, lo.y, hi.x, hi.y);
-    }
-    return make_uint2(o[0], o[1]);
-}
-
 __device__ __forceinline__ void append_lengths(const RopeAppendArgs& a) {
     if (!a.seqused_k_out) return;
     for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.B; b += gridDim.x * blockDim.x)
@@ -302,23 +334,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeApp
     const bool turns = a.r.table && u < a.r.rot / 16;
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
-    const int H = a.Hq + 2 * a.Hkv;
-    constexpr int N = 4;
-    uint4 xa[N], xb[N];
-    auto load = [&](int h0) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int h = h0 + n * a.parts * HP;
-            if (h < H) {
-                const HeadRows& x = h < a.Hq ? a.q : h < a.Hq + a.Hkv ? a.k : a.v;
-                const __nv_bfloat16* src = x.p + t * x.row + (h < a.Hq ? h : h < a.Hq + a.Hkv ? h - a.Hq : h - a.Hq - a.Hkv) * x.head;
-                xa[n] = *reinterpret_cast<const uint4*>(src + ca);
-                xb[n] = *reinterpret_cast<const uint4*>(src + cb);
-            }
-        }
-    };
-    int h0 = part * HP + lane / U;
-    load(h0);                            // in flight while the token's page and angles are looked up
+    const int first = part * HP + lane / U;
+    RopeRows<D> q, k, v;
+    q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the token's page and angles are looked up
     const NewToken nt = find_new_token(a, (int)t, lane);
     if (nt.b < 0) return;
     RopeAngles g;
@@ -329,29 +347,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeApp
         ik = __frcp_rn(__ldg(a.descale_k));
         iv = __frcp_rn(__ldg(a.descale_v));
     }
-    const long long row0 = (nt.page * kPageRows + nt.pos % kPageRows) * a.Hkv;   // cache row of KV head 0
-    while (h0 < H) {
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int h = h0 + n * a.parts * HP;
-            const bool isq = h < a.Hq, isk = !isq && h < a.Hq + a.Hkv;
-            if (h >= H || (!isq && nt.page < 0)) continue;
-            uint8_t* dst = isq   ? static_cast<uint8_t*>(a.q_out) + (t * a.Hq + h) * (D * E)
-                           : isk ? a.k_cache + (row0 + h - a.Hq) * (D * E)
-                                 : a.v_cache + (row0 + h - a.Hq - a.Hkv) * (D * E);
-            if (turns && (isq || isk)) rope_unit(xa[n], xb[n], g, a.r.interleaved);
-            if (CACHE == kCacheE4m3) {
-                const float inv = isq ? iq : isk ? ik : iv;
-                *reinterpret_cast<uint2*>(dst + ca) = bf16x8_to_e4m3(xa[n], inv);
-                *reinterpret_cast<uint2*>(dst + cb) = bf16x8_to_e4m3(xb[n], inv);
-            } else {
-                *reinterpret_cast<uint4*>(dst + 2 * ca) = xa[n];
-                *reinterpret_cast<uint4*>(dst + 2 * cb) = xb[n];
-            }
-        }
-        h0 += a.parts * HP * N;
-        load(h0);
-    }
+    const long long step = (long long)a.parts * HP * D * E;
+    q.template finish<CACHE>(static_cast<uint8_t*>(a.q_out) + ((t * a.Hq + first) * D + ca) * E, step, turns, g, a.r.interleaved, iq);
+    if (nt.page < 0) return;
+    k.start(a.k, t, a.Hkv, first, a.parts, ca, cb);
+    v.start(a.v, t, a.Hkv, first, a.parts, ca, cb);
+    const long long at = (((nt.page * kPageRows + nt.pos % kPageRows) * a.Hkv + first) * D + ca) * E;
+    k.template finish<CACHE>(a.k_cache + at, step, turns, g, a.r.interleaved, ik);
+    v.template finish<CACHE>(a.v_cache + at, step, false, g, false, iv);
 }
 
 }  // namespace attn
