@@ -20,7 +20,7 @@ attn_status_t check_rope(const float* cos_sin, int max_position, int rot_dim, co
     if (rot_dim % 16 || n_axes > kRopeMaxAxes) return ATTN_ERR_UNSUPPORTED;
     if (!positions && !optional) return ATTN_ERR_INVALID_ARG;
     if (n_axes > 1 && (!positions || !pair_axis)) return ATTN_ERR_INVALID_ARG;
-    if (!aligned16(cos_sin)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned16(cos_sin) || (n_axes > 1 && !aligned16(pair_axis))) return ATTN_ERR_INVALID_ARG;
     return ATTN_OK;
 }
 
@@ -159,7 +159,7 @@ template <int D, int GS>
 attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
     // a page and head per warp; every block builds the tables, so no more blocks than fill the GPU
     const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv;
-    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 3));
+    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 4));
     q4_gather_kernel<D, GS><<<grid, 256, 2 * (a.B + 1) * sizeof(int), st>>>(a);
     return launch_status();
 }

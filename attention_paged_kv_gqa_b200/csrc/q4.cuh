@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_q4_kernel(const Rope
         const bool turns = u < nrot;
         int ca, cb;
         rope_columns(a.r, u, &ca, &cb);
-        RopeRows<D> q;
+        RopeRows<D, 4> q;
         q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the page and the angles are looked up
         nt = find_new_token(a, (int)t, lane);
         if (nt.b < 0) return;
@@ -345,19 +345,33 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
         for (int b = threadIdx.x; b <= a.B; b += blockDim.x) a.cu_out[b] = min(rows[b], a.total);
     const long long items = (long long)pages[a.B] * a.Hkv;
     const int warps = gridDim.x * (blockDim.x >> 5);
-    for (long long it = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); it < items; it += warps) {
-        const int g = (int)(it / a.Hkv), h = (int)(it % a.Hkv);
+    struct Item {
+        int h, b, s0, slot, n, page;
+    };
+    auto look_up = [&](long long it) {
+        Item x;
+        const int g = (int)(it / a.Hkv);
+        x.h = (int)(it - (long long)g * a.Hkv);
         int lo = 0, hi = a.B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (pages[mid] <= g) lo = mid; else hi = mid;
         }
-        const int b = lo;
-        const int s0 = a.starts ? max(a.starts[b], 0) : 0;
-        const int slot = s0 / kPageRows + (g - pages[b]);
-        int n = a.cu ? a.cu[b + 1] - a.cu[b] : a.lens[b];
-        n = min(n, a.max_blocks * kPageRows - s0);
-        int page = __ldg(&a.block_table[(long long)b * a.max_blocks + slot]);
+        x.b = lo;
+        x.s0 = a.starts ? max(__ldg(&a.starts[lo]), 0) : 0;
+        x.slot = x.s0 / kPageRows + (g - pages[lo]);
+        x.n = min(a.cu ? __ldg(&a.cu[lo + 1]) - rows[lo] : a.lens[lo], a.max_blocks * kPageRows - x.s0);
+        x.page = __ldg(&a.block_table[(long long)lo * a.max_blocks + x.slot]);
+        return x;
+    };
+    long long it = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    Item next;
+    if (it < items) next = look_up(it);
+    for (; it < items; it += warps) {
+        const Item x = next;
+        if (it + warps < items) next = look_up(it + warps);      // in flight beside this one
+        const int h = x.h, b = x.b, s0 = x.s0, slot = x.slot, n = x.n;
+        int page = x.page;
         if (page < 0 || page >= a.num_blocks) {
             if (lane == 0) record_data_error(kErrDecPageRange);
             page = 0;

@@ -47,20 +47,24 @@ struct RopeAngles {
 // The eight pairs 8 u .. 8 u + 7 of token t.
 __device__ __forceinline__ RopeAngles rope_angles(const RopeTable& r, long long t, long long total, int u, int seq_pos) {
     const int half = r.rot / 2;
-    auto place = [&](int axis) {
-        int p = r.positions ? __ldg(r.positions + axis * total + t) : seq_pos;
-        if (p < 0 || p >= r.max_pos) {
-            record_data_error(kErrRopePosition);   // reported, the nearest row used
-            p = min(max(p, 0), r.max_pos - 1);
+    // the token's position on every axis, and the axes of the eight pairs
+    int p[kRopeMaxAxes];
+#pragma unroll
+    for (int a = 0; a < kRopeMaxAxes; ++a) p[a] = a < r.axes ? r.positions ? __ldg(r.positions + a * total + t) : seq_pos : 0;
+#pragma unroll
+    for (int a = 0; a < kRopeMaxAxes; ++a)
+        if (p[a] < 0 || p[a] >= r.max_pos) {
+            record_data_error(kErrRopePosition);       // reported, the nearest row used
+            p[a] = min(max(p[a], 0), r.max_pos - 1);
         }
-        return p;
-    };
     int ax[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     bool one = true;
     if (r.pair_axis) {
+        const int4 a0 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u));
+        const int4 a1 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u + 4));
+        ax[0] = a0.x, ax[1] = a0.y, ax[2] = a0.z, ax[3] = a0.w, ax[4] = a1.x, ax[5] = a1.y, ax[6] = a1.z, ax[7] = a1.w;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            ax[i] = __ldg(r.pair_axis + 8 * u + i);
             if (ax[i] < 0 || ax[i] >= r.axes) {
                 record_data_error(kErrRopeAxis);
                 ax[i] = 0;
@@ -68,6 +72,7 @@ __device__ __forceinline__ RopeAngles rope_angles(const RopeTable& r, long long 
             one = one && ax[i] == ax[0];
         }
     }
+    auto place = [&](int a) { return a == 0 ? p[0] : a == 1 ? p[1] : a == 2 ? p[2] : p[3]; };
     RopeAngles g;
     if (one) {
         const float* row = r.table + (long long)place(ax[0]) * r.rot + 8 * u;
@@ -163,9 +168,9 @@ __device__ __forceinline__ uint2 bf16x8_to_e4m3(uint4 x, float inv) {
 // One token's rows of H heads (q, k or v) on their way: a warp takes every parts-th group of
 // HP heads, a lane its unit (pieces at columns ca and cb) of each.  N groups' loads are in
 // flight together; start() issues the first ones, before the caller looks the token up.
-template <int D>
+template <int D, int N>
 struct RopeRows {
-    static constexpr int U = D / 16, HP = 32 / U, N = 4;
+    static constexpr int U = D / 16, HP = 32 / U;
     const __nv_bfloat16* src;            // this lane's first group, piece a
     long long pitch;                     // elements to its next group
     int left, apart;                     // heads from its first one on, heads between its groups
@@ -239,7 +244,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
     const int first = part * HP + lane / U;
-    RopeRows<D> q, k;
+    RopeRows<D, 4> q;
+    RopeRows<D, 2> k;
     q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the angles are looked up
     k.start(a.k, t, a.Hkv, first, a.parts, ca, cb);
     RopeAngles g;
@@ -335,7 +341,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeApp
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
     const int first = part * HP + lane / U;
-    RopeRows<D> q, k, v;
+    RopeRows<D, 4> q;
+    RopeRows<D, 2> k, v;                 // (fewer heads)
     q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the token's page and angles are looked up
     const NewToken nt = find_new_token(a, (int)t, lane);
     if (nt.b < 0) return;

@@ -455,8 +455,9 @@ attn_status_t attn_decode_paged_noalloc(
  *                  no input shares.
  *   cos_sin        fp32 [max_position, rot_dim], 16-byte aligned.
  *   positions      int32 [n_axes, total].
- *   pair_axis      int32 [rot_dim / 2]: the axis of each pair (time, height and
- *                  width of image and video tokens); not read with n_axes 1.
+ *   pair_axis      int32 [rot_dim / 2], 16-byte aligned: the axis of each pair
+ *                  (time, height and width of image and video tokens); not read
+ *                  with n_axes 1.
  * A position outside [0, max_position) is reported (code 521 of
  * attn_device_error) and the nearest row used.  Every product and sum is rounded
  * to fp32, the result to bf16.  Supported: head_dim in {64, 128}, rot_dim a

@@ -44,6 +44,7 @@ def rope(L, **kw):
     (dict(rot_dim=0), INVALID), (dict(rot_dim=144), INVALID), (dict(rot_dim=24), UNSUPPORTED),
     (dict(positions=None), INVALID), (dict(n_axes=0), INVALID), (dict(n_axes=5, pair_axis=P0), UNSUPPORTED),
     (dict(n_axes=3), INVALID),                                # axes without pair_axis
+    (dict(n_axes=3, pair_axis=P0 + 4), INVALID),
     (dict(q=P0 + 8), INVALID), (dict(k_out=P0 + 2), INVALID), (dict(sq=st(2048, 100)), INVALID),
     (dict(sko=st(2044, 128)), INVALID)])
 def test_rope_refusals(L, kw, want):
