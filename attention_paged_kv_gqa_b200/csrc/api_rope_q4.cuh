@@ -128,13 +128,18 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     using C = Q4Cfg<D, GS>;
     int ns = 0;
     while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= kQ4Smem) ++ns;
-    // a warp holds one page of a pair while it waits for the other, SUB pages on
+    // A multiple of SUB: a stage then holds the pages of the same warps in every round, so a warp
+    // that waits for a stage's next round has itself seen the one before end.  (Otherwise a warp
+    // whose pages came early would take a barrier still in the round before, for another warp's
+    // late page, for one that had passed.)  Two rounds: a warp holds one page of a pair while it
+    // waits for the other, SUB pages on.
+    ns = ns / a.SUB * a.SUB;
     if (ns < 2 * a.SUB) return ATTN_ERR_UNSUPPORTED;
     a.nstages = ns;
     const int per_row = p.spread * p.parts;
     a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;
-    q4_attn_kernel<D, GS, NT><<<grid, 32 * (q4_warps(NT) + 4), C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st>>>(a);
-    attn_status_t s = launch_status();
+    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS, NT>, dim3(grid), dim3(32 * (q4_warps(NT) + 4)),
+                                       C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st, true, a);
     if (s != ATTN_OK) return s;
     // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp
     const long long rows_out = (long long)a.B * a.max_q * a.Hq;

@@ -646,8 +646,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
     uint64_t *qfull = empty + NS, *qempty = qfull + 2;
     __shared__ int bounds[2], first_place[2];        // the share's first page and the one behind it; its first sequence
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // Launched as a programmatic dependent of whatever precedes it.  Only then may the combine
+    // kernel start, which reads the lengths before it waits for this one.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // (by way of a shuffle: what depends on the warp alone then stays off the vector units)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     auto queries = [&](int b) { return q4_queries(a, b); };

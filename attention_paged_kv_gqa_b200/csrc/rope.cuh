@@ -244,8 +244,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     int ca, cb;
     rope_columns(a.r, u, &ca, &cb);
     const int first = part * HP + lane / U;
-    RopeRows<D, 4> q;
-    RopeRows<D, 2> k;
+    RopeRows<D, D == 64 ? 2 : 4> q;      // (two groups of narrow heads are 16: at four, 22.5 us in place of 20.5
+    RopeRows<D, 2> k;                    // for 11103 tokens of 16 + 16)
     q.start(a.q, t, a.Hq, first, a.parts, ca, cb);     // in flight while the angles are looked up
     k.start(a.k, t, a.Hkv, first, a.parts, ca, cb);
     RopeAngles g;
