@@ -507,7 +507,8 @@ def attn_bwd_dense(q, k, v, o, dout, lse, *, causal=False, scale=None, window_le
 # one comparison each, with the message worked out only for a tensor that fails.
 
 _BF16, _F32, _I32, _I16, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int16, torch.uint8
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _need(ok, where, what):
@@ -554,6 +555,21 @@ def _cuda(t, where, name):
 
 
 _Strides = ctypes.c_int64 * 2
+_strides = {}              # (token, head) strides -> the array that C takes
+
+
+def _pair(row, head):
+    a = _strides.get((row, head))
+    if a is None:
+        if len(_strides) > 512:
+            _strides.clear()
+        a = _strides[row, head] = _Strides(row, head)
+    return a
+
+
+def _new_heads(t, shape):
+    """A new contiguous bf16 [rows, heads, head_dim] tensor beside t, and its strides."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format), _pair(shape[1] * shape[2], shape[2])
 
 
 def _heads(t, shape, dev, where, name):
@@ -564,7 +580,7 @@ def _heads(t, shape, dev, where, name):
     if one != 1 or (row | head) & 7 or t.data_ptr() & 15:
         raise ValueError("%s: %s needs a contiguous head_dim, strides that are multiples of 8 and a "
                          "16-byte aligned start" % (where, name))
-    return _Strides(row, head)
+    return _pair(row, head)
 
 
 def _call(fn, dev, stream, *args):
@@ -576,7 +592,7 @@ def _call(fn, dev, stream, *args):
         raw = _raw_stream(i)
     else:
         raw = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() != i:
+    if _current_device() != i:
         with torch.cuda.device(dev):
             return fn(*args, raw)
     return fn(*args, raw)
@@ -624,15 +640,17 @@ def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=Fals
     sq = _heads(q, (total, Hq, D), dev, where, "q")
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, False)
     if out_q is None:
-        out_q = q.new_empty((total, Hq, D))
-    so = _heads(out_q, (total, Hq, D), dev, where, "out_q")
+        out_q, so = _new_heads(q, (total, Hq, D))
+    else:
+        so = _heads(out_q, (total, Hq, D), dev, where, "out_q")
     Hkv, sk, sko = 0, None, None
     if k is not None:
         Hkv = _dims(k, 3, where, "k")[1]
         sk = _heads(k, (total, Hkv, D), dev, where, "k")
         if out_k is None:
-            out_k = k.new_empty((total, Hkv, D))
-        sko = _heads(out_k, (total, Hkv, D), dev, where, "out_k")
+            out_k, sko = _new_heads(k, (total, Hkv, D))
+        else:
+            sko = _heads(out_k, (total, Hkv, D), dev, where, "out_k")
     else:
         _need(out_k is None, where, "out_k without k")
     if total == 0:
@@ -652,7 +670,7 @@ def _append_args(q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, sequse
         Hq = _dims(q, 3, where, "q")[1]
         sq = _heads(q, (total, Hq, D), dev, where, "q")
         if out_q is None:
-            out_q = q.new_empty((total, Hq, D), dtype=q_dtype)
+            out_q = torch.empty_like(q, dtype=q_dtype, memory_format=torch.contiguous_format)
         else:
             _tensor(out_q, q_dtype, (total, Hq, D), dev, where, "out_q")
             _need(out_q.data_ptr() % 16 == 0, where, "out_q must be 16-byte aligned")

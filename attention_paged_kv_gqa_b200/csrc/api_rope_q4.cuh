@@ -84,6 +84,16 @@ Q4Parts q4_parts(int B, int nhb, int SUB, int grid) {
     return p;
 }
 
+// SMs of the current device; without one more than any has.
+int sm_count_or_most() {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 1024;
+    }
+    return sm_count(dev);
+}
+
 size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
     int HB, SUB;
     q4_split(Hkv, rows > 8 ? 2 : 1, &HB, &SUB);
@@ -412,7 +422,7 @@ attn_status_t attn_kv_gather_paged_q4(const void* k_cache, const void* v_cache, 
 
 size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D) {
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 16) return 0;
-    return q4_workspace(B, Hkv, D, Hq / Hkv, current_sm_count_or(1024)) + 16;
+    return q4_workspace(B, Hkv, D, Hq / Hkv, sm_count_or_most()) + 16;
 }
 
 attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const void* v_cache, const void* k_meta,
@@ -465,7 +475,7 @@ size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int 
     if (B <= 0 || max_seqlen_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || total_k < 0) return 0;
     const int group = Hq / Hkv;
     if (q4_fwd_streams(max_seqlen_q, group))
-        return q4_workspace(B, Hkv, D, max_seqlen_q * group, current_sm_count_or(1024)) + 16;
+        return q4_workspace(B, Hkv, D, max_seqlen_q * group, sm_count_or_most()) + 16;
     return 2 * (size_t)std::max(total_k, 1) * Hkv * D * 2 + (size_t)(B + 1) * sizeof(int) + 16;
 }
 

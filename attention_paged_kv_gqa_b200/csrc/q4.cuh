@@ -563,7 +563,7 @@ __device__ __forceinline__ int q4_pages(const Q4AttnArgs& a, int b) {
 // The cost of a CTA's share, PC that of all pages of one block of heads: equal ones, of a
 // pair of pages per warp at least.
 __device__ __forceinline__ int q4_share(int PC, const Q4AttnArgs& a) {
-    return max((int)(((long long)PC * a.nhb + a.grid - 1) / a.grid), 2 * a.SUB);
+    return max((int)(((uint32_t)(PC * a.nhb) + a.grid - 1) / (uint32_t)a.grid), 2 * a.SUB);   // (below 2^31)
 }
 
 // Eight query rows (row0 ..) of a KV head, for a sequence of n queries: their B fragments (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of
@@ -686,10 +686,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         // 2^31, as the host checks).  Where this CTA's share starts and ends:
         const int PC = run + kQ4Switch * with_any, share = q4_share(PC, a);
         for (int e = 0; e < 2; ++e) {
-            const long long c = (long long)(blockIdx.x + e) * share;
+            const uint32_t c = (blockIdx.x + e) * (uint32_t)share;       // (below 2^32)
             int hb = 0, at = run * a.nhb, b = 0;
-            if (c < (long long)PC * a.nhb) {
-                hb = a.nhb == 1 ? 0 : (int)c / PC;
+            if (c < (uint32_t)(PC * a.nhb)) {
+                hb = a.nhb == 1 ? 0 : c / (uint32_t)PC;
                 const int r = (int)c - hb * PC;
                 // the largest b with cost[b] <= r, 32 candidates at a time
                 for (int len = a.B; len > 1;) {
