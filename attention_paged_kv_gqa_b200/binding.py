@@ -598,6 +598,15 @@ def _call(fn, dev, stream, *args):
     return fn(*args, raw)
 
 
+def _kept(stream, *tensors):
+    """Memory taken here for a call on another stream than torch's current one is not handed out
+    again before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
 def _at(t):
     return None if t is None else t.data_ptr()
 
@@ -658,6 +667,7 @@ def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=Fals
     st = _call(lib().attn_rope, dev, stream, q.data_ptr(), out_q.data_ptr(), _at(k), _at(out_k), sq, so, sk, sko, total,
                Hq, Hkv, D, *rope, 1 if interleaved else 0, 1 if inverse else 0)
     _check(st, where)
+    _kept(stream, out_q, out_k)
     return out_q, out_k
 
 
@@ -732,6 +742,7 @@ def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, se
                seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, *rope, 1 if interleaved else 0,
                FP8_E4M3 if fp8 else BF16, _at(descale_q), _at(descale_k), _at(descale_v))
     _check(st, where)
+    _kept(stream, out_q, used)
     return out_q, used
 
 
@@ -773,6 +784,7 @@ def attn_kv_append_paged_q4(q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, b
                mbps, n, bs, _at(cu_seqlens_new), seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, gs, *rope,
                1 if interleaved else 0)
     _check(st, where)
+    _kept(stream, out_q, used)
     return out_q, used
 
 
@@ -808,6 +820,7 @@ def attn_kv_gather_paged_q4(k_cache, v_cache, k_meta, v_meta, block_table, cu_se
                v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, cu_seqlens.data_ptr(), _at(starts), B, total, Hkv,
                D, gs, out_k.data_ptr(), out_v.data_ptr())
     _check(st, where)
+    _kept(stream, out_k, out_v)
     return out_k, out_v
 
 
@@ -861,6 +874,7 @@ def attn_decode_paged_q4(q, k_cache, v_cache, k_meta, v_meta, block_table, sequs
                D, gs, _scale(scale), int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(),
                workspace.numel())
     _check(st, where)
+    _kept(stream, out, lse, workspace)
     return out, lse
 
 
@@ -892,4 +906,5 @@ def attn_fwd_varlen_paged_q4(q, k_cache, v_cache, k_meta, v_meta, *, block_table
                seqused_k.data_ptr(), B, total_q, total_k, most, Hq, Hkv, D, gs, _scale(scale), int(mask),
                int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel())
     _check(st, where)
+    _kept(stream, out, lse, workspace)
     return out, lse

@@ -245,6 +245,8 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
         return ATTN_ERR_INVALID_ARG;
     if (k && (!aligned16(k) || !aligned16(k_out) || !stride8(strides_k, 2) || !stride8(strides_k_out, 2)))
         return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)        // outputs: every head its own place
+        if (strides_q_out[i] < D || (k && strides_k_out[i] < D)) return ATTN_ERR_INVALID_ARG;
     int dev = 0;
     if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
     if (total == 0) return ATTN_OK;

@@ -46,7 +46,7 @@ def rope(L, **kw):
     (dict(n_axes=3), INVALID),                                # axes without pair_axis
     (dict(n_axes=3, pair_axis=P0 + 4), INVALID),
     (dict(q=P0 + 8), INVALID), (dict(k_out=P0 + 2), INVALID), (dict(sq=st(2048, 100)), INVALID),
-    (dict(sko=st(2044, 128)), INVALID)])
+    (dict(sko=st(2044, 128)), INVALID), (dict(sqo=st(0, 128)), INVALID), (dict(sko=st(2048, 64)), INVALID)])
 def test_rope_refusals(L, kw, want):
     assert rope(L, **kw) == want
 

@@ -382,6 +382,70 @@ def test_decode_refuses_small_workspace_and_wrong_tensors():
             A.attn_decode_paged_q4(q, *c, dbt, dl)
 
 
+def test_decode_past_4_gib_and_without_lse():
+    """Page offsets past 32 bits, in the append, the read back and the decode alike."""
+    Hkv, D, group, pool = 8, 128, 128, 540_000                 # 4.4 GB of codes each
+    big = [torch.empty(pool, Hkv, 16, D // 2, dtype=torch.uint8, device=DEV) for _ in range(2)] + \
+          [torch.empty(pool, Hkv, 16, 1, dtype=torch.int16, device=DEV) for _ in range(2)]
+    small = [torch.zeros(3, Hkv, 16, D // 2, dtype=torch.uint8, device=DEV) for _ in range(2)] + \
+            [torch.zeros(3, Hkv, 16, 1, dtype=torch.int16, device=DEV) for _ in range(2)]
+    far, near = i32([[pool - 1, 5, pool - 2]]).to(DEV), i32([[0, 1, 2]]).to(DEV)
+    k, v, q = randn((45, Hkv, D), 70).to(DEV), randn((45, Hkv, D), 71).to(DEV), randn((1, 16, D), 72).to(DEV)
+    cu, used = i32([0, 45]).to(DEV), i32([45]).to(DEV)
+    got = []
+    for cache, bt in ((big, far), (small, near)):
+        A.attn_kv_append_paged_q4(None, k, v, *cache, bt, i32([0]).to(DEV), cu_seqlens_new=cu)
+        o, none = A.attn_decode_paged_q4(q, *cache, bt, used, return_lse=False)
+        assert none is None
+        got.append((o, *A.attn_kv_gather_paged_q4(*cache, bt, cu, 45)))
+    assert A.attn_device_error() == 0
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
+def test_decode_nan_query_stays_in_its_row():
+    lens = [300, 20]
+    bt, pool = table_for(lens, seed=73)
+    cache = dev(*R.fill((pool, 2, 16, 32), 64, 74))
+    q = randn((2, 8, 64), 75)
+    want = A.attn_decode_paged_q4(q.to(DEV), *cache, bt.to(DEV), i32(lens).to(DEV))
+    q[0, 3, 7] = float("nan")
+    o, lse = A.attn_decode_paged_q4(q.to(DEV), *cache, bt.to(DEV), i32(lens).to(DEV))
+    assert torch.isnan(o[0, 3]).all() and torch.isnan(lse[0, 3])
+    keep = torch.ones(2, 8, dtype=torch.bool, device=DEV)
+    keep[0, 3] = False
+    assert torch.equal(o[keep], want[0][keep]) and torch.equal(lse[keep], want[1][keep])
+
+
+def test_calls_on_a_given_stream():
+    lens = [500, 77]
+    bt, pool = table_for(lens, seed=76)
+    cache = dev(*R.fill((pool, 2, 16, 64), 64, 77))
+    q, dbt, dl = randn((2, 8, 128), 78).to(DEV), bt.to(DEV), i32(lens).to(DEV)
+    want = A.attn_decode_paged_q4(q, *cache, dbt, dl)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = [A.attn_decode_paged_q4(q, *cache, dbt, dl, stream=s) for _ in range(8)]
+    outs += [A.attn_fwd_varlen_paged_q4(q, *cache, block_table=dbt, cu_seqlens_q=i32([0, 1, 2]).to(DEV), max_seqlen_q=9,
+                                        seqused_k=dl, total_k=577, mask=A.MASK_CAUSAL, stream=s)]
+    s.synchronize()
+    for o, lse in outs[:-1]:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    # the packed path (its own rounding of the probabilities): its tolerances
+    assert float((outs[-1][0].float() - want[0].float()).abs().max()) <= TOL_O_PACKED
+    assert float((outs[-1][1] - want[1].t()).abs().max()) <= TOL_LSE_PACKED
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64)])
+@pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 2), (12, 12), (32, 8)])
+def test_decode_many_short_sequences(D, group, Hq, Hkv):
+    """Shares that hold many sequences, some without keys: partials per warp, and their joins."""
+    g = torch.Generator().manual_seed(Hq)
+    lens = [int(n) for n in torch.randint(0, 60, (170,), generator=g)]
+    lens[5:9] = [0, 0, 0, 1]
+    run_decode(lens, Hq, Hkv, D, group, seed=80 + Hq)
+
+
 # ---------------------------------------------------------------- several queries
 def run_fwd(lens, qs, Hq, Hkv, D, group, causal=True, window=-1, softcap=0.0, seed=0, total_k=None):
     bt, pool = table_for(lens, seed=seed)
