@@ -978,7 +978,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + (nt * W + w) * 512);
-                    if (w == g * WG) {
+                    if (WG == 1) {
+                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
+                        q4_mma(raw[nt], hi, qw.z, qw.w);
+                    } else if (w == g * WG) {
                         q4_mma_first(raw[nt], lo, qw.x, qw.y);
                         q4_mma_first(raw2[nt], hi, qw.z, qw.w);
                     } else {
@@ -990,10 +993,12 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
             const float s0 = q4_step(km0[g]), s1 = q4_step(km1[g]), z0 = q4_zero(km0[g]), z1 = q4_zero(km1[g]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float2 y0 = ffma2(make_float2(z0, z0), qs[nt][g],
-                                        fadd2(make_float2(raw[nt][0], raw[nt][1]), make_float2(raw2[nt][0], raw2[nt][1])));
-                const float2 y1 = ffma2(make_float2(z1, z1), qs[nt][g],
-                                        fadd2(make_float2(raw[nt][2], raw[nt][3]), make_float2(raw2[nt][2], raw2[nt][3])));
+                float2 d0 = make_float2(raw[nt][0], raw[nt][1]), d1 = make_float2(raw[nt][2], raw[nt][3]);
+                if (WG > 1) {
+                    d0 = fadd2(d0, make_float2(raw2[nt][0], raw2[nt][1]));
+                    d1 = fadd2(d1, make_float2(raw2[nt][2], raw2[nt][3]));
+                }
+                const float2 y0 = ffma2(make_float2(z0, z0), qs[nt][g], d0), y1 = ffma2(make_float2(z1, z1), qs[nt][g], d1);
                 sc[nt][0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[nt][0]);
                 sc[nt][1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[nt][1]);
             }
