@@ -56,15 +56,14 @@ int rope_parts(long long tokens, int passes, int sms) {
 
 constexpr int kQ4Smem = 227 * 1024 - 256;      // (some is static)
 
-// KV heads of a CTA's block, and warps of a head: the block with the most of the CTA's
-// warps at work, the largest such one (its copies are longest).
-void q4_split(int Hkv, int NT, int* HB, int* SUB) {
-    const int warps = q4_warps(NT);
+// KV heads of a CTA's block, and warps of a head and row tile: the block with the most of
+// the CTA's warps at work, the largest such one (its copies are longest).
+void q4_split(int Hkv, int RT, int* HB, int* SUB) {
     int best = 1;
-    for (int hb = 2; hb <= std::min(Hkv, warps); ++hb)
-        if (Hkv % hb == 0 && hb * (warps / hb) >= best * (warps / best)) best = hb;
+    for (int hb = 2; hb <= std::min(Hkv, kQ4Warps / RT); ++hb)
+        if (Hkv % hb == 0 && hb * (kQ4Warps / (hb * RT)) >= best * (kQ4Warps / (best * RT))) best = hb;
     *HB = best;
-    *SUB = warps / best;
+    *SUB = kQ4Warps / (best * RT);
 }
 
 // How the partial results of a call are laid out: `slots` of (CTA, sequence and block of
@@ -96,7 +95,7 @@ int sm_count_or_most() {
 
 size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
     int HB, SUB;
-    q4_split(Hkv, rows > 8 ? 2 : 1, &HB, &SUB);
+    q4_split(Hkv, (rows + 7) / 8, &HB, &SUB);
     size_t most = 0;                       // (the grid may be smaller than the number of SMs)
     for (int grid : {sms, std::min(sms, (Hkv / HB) * B * 9)}) {
         const Q4Parts p = q4_parts(B, Hkv / HB, SUB, grid);
@@ -109,24 +108,26 @@ bool q4_group_ok(int group_size, int D) {
     return (group_size == 32 || group_size == 64 || group_size == 128) && group_size <= D;
 }
 
-template <int D, int GS, int NT>
-attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+template <int D, int GS>
+attn_status_t launch_q4_rows(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
     static std::atomic<uint64_t> attr_mask{0};   // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_mask.load() & bit)) {
-        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, NT>, kQ4Smem);
+        const attn_status_t s = set_smem(q4_attn_kernel<D, GS>, kQ4Smem);
         if (s != ATTN_OK) return s;
         attr_mask.fetch_or(bit);
     }
-    q4_split(a.Hkv, NT, &a.HB, &a.SUB);
+    a.rows = a.max_q * a.group;
+    a.RT = (a.rows + 7) / 8;
+    q4_split(a.Hkv, a.RT, &a.HB, &a.SUB);
+    const int U = a.HB * a.RT;
     a.nhb = a.Hkv / a.HB;
     const long long bound = (long long)a.B * (a.max_blocks + kQ4Switch) * a.nhb;    // of the cost
     if (bound >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     const int grid = (int)std::min<long long>(sms, bound);
     const Q4Parts p = q4_parts(a.B, a.nhb, a.SUB, grid);
-    a.rows = a.max_q * a.group;
     a.parts = p.parts;
     const size_t rows = p.slots * p.parts * a.HB * a.rows;
     if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
@@ -137,7 +138,7 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     a.grid = grid;
     using C = Q4Cfg<D, GS>;
     int ns = 0;
-    while (ns < 64 && C::smem_bytes(a.HB, a.SUB, NT, a.B, ns + 1) <= kQ4Smem) ++ns;
+    while (ns < 64 && C::smem_bytes(a.HB, U, a.SUB, a.B, ns + 1) <= kQ4Smem) ++ns;
     // A multiple of SUB: a stage then holds the pages of the same warps in every round, so a warp
     // that waits for a stage's next round has itself seen the one before end.  (Otherwise a warp
     // whose pages came early would take a barrier still in the round before, for another warp's
@@ -148,18 +149,12 @@ attn_status_t launch_q4_attn(Q4AttnArgs a, int sms, void* workspace, size_t work
     a.nstages = ns;
     const int per_row = p.spread * p.parts;
     a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;
-    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS, NT>, dim3(grid), dim3(32 * (q4_warps(NT) + 4)),
-                                       C::smem_bytes(a.HB, a.SUB, NT, a.B, ns), st, true, a);
+    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS>, dim3(grid), dim3(kQ4Threads),
+                                       C::smem_bytes(a.HB, U, a.SUB, a.B, ns), st, true, a);
     if (s != ATTN_OK) return s;
     // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp
     const long long rows_out = (long long)a.B * a.max_q * a.Hq;
     return launch_maybe_pdl(q4_combine_kernel<D>, dim3((unsigned)((rows_out * a.wpr + 7) / 8)), dim3(256), 0, st, true, a);
-}
-
-template <int D, int GS>
-attn_status_t launch_q4_rows(const Q4AttnArgs& a, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
-    return a.max_q * a.group > 8 ? launch_q4_attn<D, GS, 2>(a, sms, ws, ws_bytes, st)
-                                 : launch_q4_attn<D, GS, 1>(a, sms, ws, ws_bytes, st);
 }
 
 attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -423,7 +418,7 @@ attn_status_t attn_kv_gather_paged_q4(const void* k_cache, const void* v_cache, 
 }
 
 size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D) {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 16) return 0;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 8 * kQ4Tiles) return 0;
     return q4_workspace(B, Hkv, D, Hq / Hkv, sm_count_or_most()) + 16;
 }
 
@@ -438,7 +433,7 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
     if (s != ATTN_OK) return s;
     if ((s = check_score_mods(ATTN_MASK_CAUSAL, window_left, softcap)) != ATTN_OK) return s;
     if (Hq <= 0 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
-    if (Hq / Hkv > 16) return ATTN_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 8 * kQ4Tiles) return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
     int dev = 0;
     if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
@@ -469,9 +464,11 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
     return launch_q4(a, D, group_size, sm_count(dev), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
-// The page stream serves up to 16 query rows per KV head; above that the pages are
-// read back as packed bf16 rows (exact) and the tensor-core forward runs on those.
-static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= 16; }
+// The page stream serves up to eight tiles of eight query rows per KV head (16 sequences of
+// 3688 keys on average, groups of four: 104 us with 9 queries and 157 with 16); above that the
+// pages are read back as packed bf16 rows (exact) and the tensor-core forward runs on those
+// (235 us with 17).
+static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= 8 * kQ4Tiles; }
 
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int D, int total_k) {
     if (B <= 0 || max_seqlen_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || total_k < 0) return 0;

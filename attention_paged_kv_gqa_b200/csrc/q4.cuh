@@ -439,14 +439,14 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 }
 
 // ---------------------------------------------------------------- attention
-// A few query rows per sequence (R = tokens x query heads of a KV head <= 8 NT)
-// over 4-bit pages: the page stream of decode.cuh with another consumer.
+// A few query rows per sequence (tokens x query heads of a KV head, in RT tiles of
+// eight) over 4-bit pages: the page stream of decode.cuh with another consumer.
 //
 // The pages of the batch, for one block of HB KV heads after another, are cut
 // into one contiguous equal share per CTA.  A page's HB tiles of K, V and their
 // metas are four contiguous runs, fetched by four bulk copies into a ring of
-// stages.  Of the SUB warps of a KV head each takes every SUB-th page and keeps an
-// online softmax of its own; where a sequence or the share ends they are joined
+// stages.  Of the SUB warps of a KV head and row tile each takes every SUB-th page and
+// keeps an online softmax of its own; where a sequence or the share ends they are joined
 // through shared memory, and the partial (O normalised, LSE) goes to slot
 // CTA + sequence for the combine kernel.
 //
@@ -465,18 +465,18 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // shows by one vote.
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
 constexpr int kQ4Recentre = 16;          // pages
-// Consumer warps of a CTA: as many as have the registers for 8 NT rows (and producer
-// warps for K, V, their metas and the queries).
-__host__ __device__ constexpr int q4_warps(int NT) { return NT == 1 ? 12 : 8; }
+constexpr int kQ4Warps = 12;             // consumer warps of a CTA; and producer warps for K, V, their metas, the queries
+constexpr int kQ4Threads = 32 * (kQ4Warps + 4);
+constexpr int kQ4Tiles = 8;              // row tiles at most
 constexpr int kQ4Switch = 13;            // pages that a change of sequence costs a CTA (for equal shares)
 constexpr float kQ4NoMax = -3.0e38f;     // the maximum before the first key (finite: differences with it stay numbers)
 
 struct Q4AttnArgs {
     int B, Hq, Hkv, group;
-    int HB, SUB, nhb;        // KV heads of a block, warps of a head, blocks
+    int HB, RT, SUB, nhb;    // KV heads of a block, row tiles, warps of a head and tile, blocks
     const __nv_bfloat16* q;  // rows of queries [..][Hq][D]
     const int* cu_q;         // [B + 1], or null: one query per sequence
-    int max_q;               // query tokens a sequence may have (group * max_q <= 8 NT)
+    int max_q;               // query tokens a sequence may have (group * max_q <= 8 RT)
     int total_q;
     const uint8_t *k_cache, *v_cache;
     const uint16_t *k_meta, *v_meta;
@@ -503,18 +503,18 @@ struct Q4Cfg {
     static constexpr int TILE = kPageRows * D / 2;              // bytes of a head's K or V tile
     static constexpr int META = kPageRows * (D / GS) * 2;       // bytes of its metas
     __host__ __device__ static constexpr int stage_bytes(int HB) { return 2 * HB * (TILE + META); }
-    __host__ __device__ static constexpr int merge_bytes(int HB, int SUB, int NT) {
-        // per exchange slot: the accumulators of a warp, its maxima, sums and beta
-        return SUB > 1 ? HB * ((SUB + 1) / 2) * 32 * (D / 16 * NT * 4 + NT * 4 + 2) * 4 : 0;
+    static constexpr int PAIRS = D / 16 * 2 + 3;                // a lane exchanges: accumulators, maxima, sums, beta
+    // (U: heads x row tiles)
+    __host__ __device__ static constexpr int merge_bytes(int U, int SUB) {
+        return SUB > 1 ? U * ((SUB + 1) / 2) * 32 * PAIRS * 8 : 0;
     }
     // the queries of a segment, twice: the B fragments of Q^T, then per row the units and sums
     static constexpr int QROWS = 1 + D / GS;
-    __host__ __device__ static constexpr int query_bytes(int HB, int NT) {
-        return HB * (NT * (D / 32) * 512 + QROWS * 8 * NT * 4);
-    }
+    static constexpr int FRAG = D / 32 * 512;
+    __host__ __device__ static constexpr int query_bytes(int U) { return U * (FRAG + QROWS * 32); }
     __host__ __device__ static constexpr int table_bytes(int B) { return ((3 * B + 2) * 4 + 15) / 16 * 16; }
-    __host__ __device__ static constexpr int smem_bytes(int HB, int SUB, int NT, int B, int ns) {
-        return ns * stage_bytes(HB) + 2 * query_bytes(HB, NT) + merge_bytes(HB, SUB, NT) + table_bytes(B) + (2 * ns + 4) * 8;
+    __host__ __device__ static constexpr int smem_bytes(int HB, int U, int SUB, int B, int ns) {
+        return ns * stage_bytes(HB) + 2 * query_bytes(U) + merge_bytes(U, SUB) + table_bytes(B) + (2 * ns + 4) * 8;
     }
 };
 
@@ -566,10 +566,11 @@ __device__ __forceinline__ int q4_share(int PC, const Q4AttnArgs& a) {
     return max((int)(((uint32_t)(PC * a.nhb) + a.grid - 1) / (uint32_t)a.grid), 2 * a.SUB);   // (below 2^31)
 }
 
-// Eight query rows (row0 ..) of a KV head, for a sequence of n queries: their B fragments (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of
-// each word in f16 (second nibbles' dims over 16), and per row the unit of its raw scores in
-// log2 units and minus the sums of q over the groups.  Rows past the last query are zero.
-template <int D, int GS, int NT>
+// Eight query rows (row0 ..) of a KV head, for a sequence of n queries: their B fragments
+// (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word in f16 (second nibbles' dims over
+// 16), and per row the unit of its raw scores in log2 units and minus the sums of q over
+// the groups.  Rows past the last query are zero.
+template <int D, int GS>
 __device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int group, float unit, int n, int row0, uint32_t frag_at,
                                         uint32_t rows_at) {
     // (q: the first query of the sequence, at the KV head's first query head; offsets in shared memory)
@@ -615,29 +616,29 @@ __device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int grou
                                          pack_f16(bf16_lo(x[w].y) * up, bf16_lo(x[w].w) * up),
                                          pack_f16(bf16_hi(x[w].y) * up1, bf16_hi(x[w].w) * up1));
     if (t4 == 0) {
-        rows[row] = down * unit;
+        rows[r8] = down * unit;
 #pragma unroll
-        for (int g = 0; g < G; ++g) rows[(1 + g) * 8 * NT + row] = -sum[g] / down;
+        for (int g = 0; g < G; ++g) rows[(1 + g) * 8 + r8] = -sum[g] / down;
     }
 }
 
-template <int D, int GS, int NT>
-__global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(const Q4AttnArgs a) {
+template <int D, int GS>
+__global__ void __launch_bounds__(kQ4Threads, 1) q4_attn_kernel(const Q4AttnArgs a) {
     using C = Q4Cfg<D, GS>;
     constexpr int W = D / 32;            // words of a lane's K row piece; V words per token pair
     constexpr int G = D / GS;            // groups of a head
     constexpr int WG = W / G;            // words of a group
     constexpr int MT = D / 16;           // 16-column output tiles
-    constexpr int NP = NT == 1 ? 2 : 1;  // pages a warp takes at once: two chains of dependent operations side by side
-    const int NS = a.nstages, HB = a.HB, SUB = a.SUB, SB = C::stage_bytes(HB);
+    constexpr int NP = 2;                // pages a warp takes at once: two chains of dependent operations side by side
+    const int NS = a.nstages, HB = a.HB, SUB = a.SUB, U = HB * a.RT, SB = C::stage_bytes(HB);
     extern __shared__ __align__(128) uint8_t q4_smem[];
     uint8_t* smem = q4_smem;
     uint8_t* tail = smem + NS * SB;
-    uint8_t* qarea = tail;                           // two of: [HB][NT][W][32] uint4, [HB][QROWS][8 NT] float
-    const int QB = C::query_bytes(HB, NT);
+    uint8_t* qarea = tail;                           // two of: [U][W][32] uint4, [U][QROWS][8] float
+    const int QB = C::query_bytes(U);
     tail += 2 * QB;
     float* mrg = reinterpret_cast<float*>(tail);
-    tail += C::merge_bytes(HB, SUB, NT);
+    tail += C::merge_bytes(U, SUB);
     int* prefix = reinterpret_cast<int*>(tail);      // [B + 1] pages before sequence b
     int* cost = prefix + (a.B + 1);                  // [B + 1] their cost
     int* lenv = cost + (a.B + 1);                    // [B]
@@ -712,11 +713,11 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
     if (threadIdx.x == 32) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], 3);
-            mbar_init(&empty[i], HB);
+            mbar_init(&empty[i], U);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&qfull[i], 1);
-            mbar_init(&qempty[i], HB * SUB);
+            mbar_init(&qempty[i], U * SUB);
         }
         fence_mbar_init();
     }
@@ -731,9 +732,9 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         const uint32_t to = (uint32_t)(qarea - smem) + (turn & 1) * QB;
         const __nv_bfloat16* q = a.q + ((long long)(a.cu_q ? __ldg(&a.cu_q[b]) : b) * a.Hq + hb * HB * a.group) * D;
         const int n = queries(b);
-        for (int t = first; t < HB * NT; t += step)
-            q4_prepare<D, GS, NT>(q + t / NT * a.group * D, a.Hq, a.group, a.scale * kLog2e, n, t % NT * 8, to + t * W * 512,
-                                  to + HB * NT * W * 512 + t / NT * C::QROWS * 32 * NT);
+        for (int t = first; t < U; t += step)
+            q4_prepare<D, GS>(q + t / a.RT * a.group * D, a.Hq, a.group, a.scale * kLog2e, n, t % a.RT * 8, to + t * C::FRAG,
+                              to + U * C::FRAG + t * C::QROWS * 32);
     };
     // The sequences of the share in order: (block of heads, sequence), and the page at which each ends.
     struct Place {
@@ -752,9 +753,9 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
     };
     const Place start = {first_place[0], first_place[1], ends(first_place[0], first_place[1])};
 
-    if (warp >= q4_warps(NT)) {
+    if (warp >= kQ4Warps) {
         // ------------------------------------------------------------ producers: K, V, metas, queries
-        const int which = warp - q4_warps(NT);
+        const int which = warp - kQ4Warps;
         if (which == 3) {
             Place x = start;
             for (int turn = 1; x.end < npages; ++turn) {
@@ -815,38 +816,34 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         }
         return;
     }
-    if (warp >= HB * SUB) return;
+    if (warp >= U * SUB) return;
     // ---------------------------------------------------------------- consumers
-    const int h = warp / SUB, sub = warp % SUB;      // head of the block, this warp's share of its pages
+    const int unit = warp / SUB, sub = warp % SUB;   // head and row tile, this warp's share of their pages
+    const int h = unit / a.RT, row0 = unit % a.RT * 8;
     const int r8 = lane >> 2, t4 = lane & 3;
     const bool capped = a.softcap > 0.0f;
     // this lane's B fragments of Q^T, (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word: in
     // shared memory, which spares registers
     uint32_t qb = 0;                     // (its offset in shared memory)
     // of the columns 2 t4 and 2 t4 + 1 (x, y) of each 8-row tile:
-    float2 qs[NT][G];                    // minus the sum of q over a group, in units of the raw score
-    float2 kf[NT];                       // score in log2 units = raw score * kf
-    float2 acc[MT][NT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
-    float2 zac[NT][G];                   // sum w zero, this lane's keys
-    float2 m[NT], l[NT];                 // minus the maximum (log2 units); sum, this lane's keys
-    float2 thr[NT];                      // the raw score that moves the maximum
+    float2 qs[G];                    // minus the sum of q over a group, in units of the raw score
+    float2 kf;                       // score in log2 units = raw score * kf
+    float2 acc[MT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
+    float2 zac[G];                   // sum w zero, this lane's keys
+    float2 m, l;                 // minus the maximum (log2 units); sum, this lane's keys
+    float2 thr;                      // the raw score that moves the maximum
     float beta = 1.0f;                   // w = p step beta
     uint32_t cap_meta = 0;               // metas below it have steps that beta keeps in range
     int since = 0;
     auto reset = [&]() {
         const float2 zero2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int c = 0; c < MT; ++c)
+        for (int c = 0; c < MT; ++c) acc[c][0] = acc[c][1] = zero2;
+        m = make_float2(-kQ4NoMax, -kQ4NoMax);
+        thr = make_float2(-INFINITY, -INFINITY);
+        l = zero2;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[c][nt][0] = acc[c][nt][1] = zero2;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt] = make_float2(-kQ4NoMax, -kQ4NoMax);
-            thr[nt] = make_float2(-INFINITY, -INFINITY);
-            l[nt] = zero2;
-#pragma unroll
-            for (int g = 0; g < G; ++g) zac[nt][g] = zero2;
-        }
+        for (int g = 0; g < G; ++g) zac[g] = zero2;
         beta = 1.0f;
         cap_meta = 16;                               // a step above zero
         since = 0;
@@ -862,93 +859,80 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
     // takes sum w zero out of the accumulators
     auto recentre = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int g = 0; g < G; ++g) {
+            const float2 z = over_rows(zac[g]);
+            zac[g] = make_float2(0.0f, 0.0f);
+            const float lo = -5.9604644775390625e-8f, hi = -9.5367431640625e-7f;     // -2^-24, -2^-20
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const float2 z = over_rows(zac[nt][g]);
-                zac[nt][g] = make_float2(0.0f, 0.0f);
-                const float lo = -5.9604644775390625e-8f, hi = -9.5367431640625e-7f;     // -2^-24, -2^-20
-#pragma unroll
-                for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
-                    acc[c][nt][0] = ffma2(z, make_float2(lo, lo), acc[c][nt][0]);
-                    acc[c][nt][1] = ffma2(z, make_float2(hi, hi), acc[c][nt][1]);
-                }
+            for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
+                acc[c][0] = ffma2(z, make_float2(lo, lo), acc[c][0]);
+                acc[c][1] = ffma2(z, make_float2(hi, hi), acc[c][1]);
             }
+        }
         since = 0;
     };
     // the end of a sequence or of the share: join the SUB warps of the head, write the partial
     auto flush_partial = [&](int vb, int n) {
         recentre();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) l[nt] = over_rows(l[nt]);
-        constexpr int FL = MT * NT * 2 + NT * 2 + 1; // pairs a lane exchanges
+        l = over_rows(l);
+        constexpr int FL = C::PAIRS;                 // pairs a lane exchanges
         const int slots = (SUB + 1) / 2;
-        float2* mine = reinterpret_cast<float2*>(mrg) + h * slots * 32 * FL;
+        float2* mine = reinterpret_cast<float2*>(mrg) + unit * slots * 32 * FL;
         int width = 1;
         while (width < SUB && a.parts == 1) width <<= 1;
         for (int st = width / 2; st > 0; st >>= 1) {
             if (sub >= st && sub < 2 * st) {
                 float2* x = mine + (sub - st) * 32 * FL + lane;
 #pragma unroll
-                for (int c = 0; c < MT; ++c)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        x[32 * (c * NT + nt) * 2] = acc[c][nt][0];
-                        x[32 * ((c * NT + nt) * 2 + 1)] = acc[c][nt][1];
-                    }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    x[32 * (MT * NT + nt) * 2] = m[nt];
-                    x[32 * ((MT * NT + nt) * 2 + 1)] = l[nt];
+                for (int c = 0; c < MT; ++c) {
+                    x[32 * (2 * c)] = acc[c][0];
+                    x[32 * (2 * c + 1)] = acc[c][1];
                 }
-                x[32 * (FL - 1)] = make_float2(beta, 0.0f);
+                x[32 * (2 * MT)] = m;
+                x[32 * (2 * MT + 1)] = l;
+                x[32 * (2 * MT + 2)] = make_float2(beta, 0.0f);
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + h), "r"(32 * SUB) : "memory");
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
             if (sub < st && sub + st < SUB) {
                 const float2* x = mine + sub * 32 * FL + lane;
-                const float beta2 = x[32 * (FL - 1)].x, nb = fminf(beta, beta2);     // the larger steps' unit
+                const float beta2 = x[32 * (2 * MT + 2)].x, nb = fminf(beta, beta2);     // the larger steps' unit
                 const float r1 = nb / beta, r2 = nb / beta2;
                 beta = nb;
+                const float2 m2 = x[32 * (2 * MT)], l2 = x[32 * (2 * MT + 1)];
+                const float2 mn = make_float2(fminf(m.x, m2.x), fminf(m.y, m2.y));
+                float2 f1 = make_float2(ex2(mn.x - m.x), ex2(mn.y - m.y));
+                float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
+                m = mn;
+                l = ffma2(l, f1, fmul2(l2, f2));
+                f1 = fmul2(f1, make_float2(r1, r1));
+                f2 = fmul2(f2, make_float2(r2, r2));
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float2 m2 = x[32 * (MT * NT + nt) * 2], l2 = x[32 * ((MT * NT + nt) * 2 + 1)];
-                    const float2 mn = make_float2(fminf(m[nt].x, m2.x), fminf(m[nt].y, m2.y));
-                    float2 f1 = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
-                    float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
-                    m[nt] = mn;
-                    l[nt] = ffma2(l[nt], f1, fmul2(l2, f2));
-                    f1 = fmul2(f1, make_float2(r1, r1));
-                    f2 = fmul2(f2, make_float2(r2, r2));
+                for (int c = 0; c < MT; ++c)
 #pragma unroll
-                    for (int c = 0; c < MT; ++c)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            acc[c][nt][y] = ffma2(acc[c][nt][y], f1, fmul2(x[32 * ((c * NT + nt) * 2 + y)], f2));
-                }
+                    for (int y = 0; y < 2; ++y)
+                        acc[c][y] = ffma2(acc[c][y], f1, fmul2(x[32 * (2 * c + y)], f2));
             }
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + h), "r"(32 * SUB) : "memory");
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
         }
         if (sub >= a.parts) return;
         const float back = 64.0f / beta;             // a power of two, within range for every step
-        const long long row0 = ((((long long)blockIdx.x + vb) * a.parts + sub) * HB + h) * a.rows;
+        const long long base = ((((long long)blockIdx.x + vb) * a.parts + sub) * HB + h) * a.rows;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 2; ++e) {
+            const int row = row0 + 2 * t4 + e;
+            if (row >= n * a.group) continue;
+            const float s = e ? l.y : l.x;
+            const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
+            const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
+            float* rp = a.o_part + (base + row) * D;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = nt * 8 + 2 * t4 + e;
-                if (row >= n * a.group) continue;
-                const float s = e ? l[nt].y : l[nt].x;
-                const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
-                const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
-                float* rp = a.o_part + (row0 + row) * D;
-#pragma unroll
-                for (int c = 0; c < MT; ++c) {
-                    rp[16 * c + r8] = (e ? acc[c][nt][0].y : acc[c][nt][0].x) * lo * back;
-                    rp[16 * c + 8 + r8] = (e ? acc[c][nt][1].y : acc[c][nt][1].x) * hi * back;
-                }
-                if (r8 == 0)
-                    a.lse_part[row0 + row] = s > 0.0f ? (log2f(s) - (e ? m[nt].y : m[nt].x)) * kLn2 : s == s ? -INFINITY : s;
+            for (int c = 0; c < MT; ++c) {
+                rp[16 * c + r8] = (e ? acc[c][0].y : acc[c][0].x) * lo * back;
+                rp[16 * c + 8 + r8] = (e ? acc[c][1].y : acc[c][1].x) * hi * back;
             }
+            if (r8 == 0)
+                a.lse_part[base + row] = s > 0.0f ? (log2f(s) - (e ? m.y : m.x)) * kLn2 : s == s ? -INFINITY : s;
+        }
     };
     bool ok = true;
     int i = sub, st = sub;                           // this warp's next page of the share, and its stage
@@ -961,7 +945,7 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
     const uint8_t* vbase = smem + (HB + h) * C::TILE + lane * W * 4;
     const uint8_t* mbase = smem + 2 * HB * C::TILE + h * C::META + r8 * G * 2;
     // raw scores of a page's keys r8 and r8 + 8 against the tile's columns
-    auto scores = [&](int so, float2 (&sc)[NT][2]) {
+    auto scores = [&](int so, float2 (&sc)[2]) {
         uint32_t k0[W], k1[W], km0[G], km1[G];
         load_words<W>(kbase + so, k0);
         load_words<W>(kbase + so + 4 * D, k1);
@@ -969,39 +953,33 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         load_metas<G>(mbase + so + 16 * G, km1);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float raw[NT][4], raw2[NT][4];
+            float raw[4], raw2[4];
 #pragma unroll
             for (int w = g * WG; w < (g + 1) * WG; ++w) {
                 const uint32_t lo[4] = {k0[w] & 0x000f000fu, k1[w] & 0x000f000fu, k0[w] & 0x00f000f0u, k1[w] & 0x00f000f0u};
                 const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
                 const uint32_t hi[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + (nt * W + w) * 512);
-                    if (WG == 1) {
-                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
-                        q4_mma(raw[nt], hi, qw.z, qw.w);
-                    } else if (w == g * WG) {
-                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
-                        q4_mma_first(raw2[nt], hi, qw.z, qw.w);
-                    } else {
-                        q4_mma(raw[nt], lo, qw.x, qw.y);
-                        q4_mma(raw2[nt], hi, qw.z, qw.w);
-                    }
+                const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + w * 512);
+                if (WG == 1) {
+                    q4_mma_first(raw, lo, qw.x, qw.y);
+                    q4_mma(raw, hi, qw.z, qw.w);
+                } else if (w == g * WG) {
+                    q4_mma_first(raw, lo, qw.x, qw.y);
+                    q4_mma_first(raw2, hi, qw.z, qw.w);
+                } else {
+                    q4_mma(raw, lo, qw.x, qw.y);
+                    q4_mma(raw2, hi, qw.z, qw.w);
                 }
             }
             const float s0 = q4_step(km0[g]), s1 = q4_step(km1[g]), z0 = q4_zero(km0[g]), z1 = q4_zero(km1[g]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float2 d0 = make_float2(raw[nt][0], raw[nt][1]), d1 = make_float2(raw[nt][2], raw[nt][3]);
-                if (WG > 1) {
-                    d0 = fadd2(d0, make_float2(raw2[nt][0], raw2[nt][1]));
-                    d1 = fadd2(d1, make_float2(raw2[nt][2], raw2[nt][3]));
-                }
-                const float2 y0 = ffma2(make_float2(z0, z0), qs[nt][g], d0), y1 = ffma2(make_float2(z1, z1), qs[nt][g], d1);
-                sc[nt][0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[nt][0]);
-                sc[nt][1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[nt][1]);
+            float2 d0 = make_float2(raw[0], raw[1]), d1 = make_float2(raw[2], raw[3]);
+            if (WG > 1) {
+                d0 = fadd2(d0, make_float2(raw2[0], raw2[1]));
+                d1 = fadd2(d1, make_float2(raw2[2], raw2[3]));
             }
+            const float2 y0 = ffma2(make_float2(z0, z0), qs[g], d0), y1 = ffma2(make_float2(z1, z1), qs[g], d1);
+            sc[0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[0]);
+            sc[1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[1]);
         }
     };
     int turn = 0;                                    // sequences of the share so far
@@ -1014,29 +992,26 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
         const int key0 = (g0 - prefix[b] + q4_first_key(L, n, a.window) / kPageRows) * kPageRows;
         reset();
         if (turn == 0) {
-            prepare(0, hb, b, warp, HB * SUB);
-            asm volatile("bar.sync 15, %0;" ::"r"(32 * HB * SUB) : "memory");
+            prepare(0, hb, b, warp, U * SUB);
+            asm volatile("bar.sync 15, %0;" ::"r"(32 * U * SUB) : "memory");
         } else if (ok) {
             ok = mbar_wait(&qfull[turn & 1], (turn >> 1 & 1) ^ (turn & 1 ^ 1), kErrQ4Full);
             ok = __all_sync(0xffffffffu, ok);
         }
         {
             const uint8_t* q = qarea + (turn & 1) * QB;
-            qb = (uint32_t)(qarea - smem) + (turn & 1) * QB + (h * NT * W * 32 + lane) * 16;
-            const float* rows = reinterpret_cast<const float*>(q + HB * NT * W * 512) + h * C::QROWS * 8 * NT + 2 * t4;
+            qb = (uint32_t)(qarea - smem) + (turn & 1) * QB + unit * C::FRAG + lane * 16;
+            const float* rows = reinterpret_cast<const float*>(q + U * C::FRAG) + unit * C::QROWS * 8 + 2 * t4;
+            kf = *reinterpret_cast<const float2*>(rows);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                kf[nt] = *reinterpret_cast<const float2*>(rows + 8 * nt);
-#pragma unroll
-                for (int g = 0; g < G; ++g) qs[nt][g] = *reinterpret_cast<const float2*>(rows + (1 + g) * 8 * NT + 8 * nt);
-            }
+            for (int g = 0; g < G; ++g) qs[g] = *reinterpret_cast<const float2*>(rows + (1 + g) * 8);
         }
         // pages whose keys every query sees: key0 of the page in [all_lo, all_hi]
         const int all_hi = (a.causal ? L - n : L - 1) - (kPageRows - 1);
         const int all_lo = a.window >= 0 ? L - 1 - a.window : 0;
         // waits for this warp's next page (and the one after); their stages go to `at`
         auto take = [&](int (&at)[NP]) {
-            const bool two = NP > 1 && i + SUB < seg_end;
+            const bool two = i + SUB < seg_end;
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
                 if (x == 0 || two) {
@@ -1058,7 +1033,7 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
             return two;
         };
         int at[NP];
-        float2 sc[NP][NT][2];
+        float2 sc[NP][2];
         while (i < seg_end) {
             const int tok0 = key0 + (i - seg) * kPageRows;
             const bool two = take(at);
@@ -1071,18 +1046,15 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
                 load_metas<G>(mbase + at[x] * SB + HB * C::META + 16 * G, vm1[x]);
             }
             if (capped) {
+                const float b0 = kf.x * kLn2, b1 = kf.y * kLn2;             // to natural units
+                const float i0 = b0 / a.softcap, i1 = b1 / a.softcap, o0 = a.softcap / b0, o1 = a.softcap / b1;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float b0 = kf[nt].x * kLn2, b1 = kf[nt].y * kLn2;             // to natural units
-                    const float i0 = b0 / a.softcap, i1 = b1 / a.softcap, o0 = a.softcap / b0, o1 = a.softcap / b1;
+                for (int x = 0; x < NP; ++x)
 #pragma unroll
-                    for (int x = 0; x < NP; ++x)
-#pragma unroll
-                        for (int y = 0; y < 2; ++y)
-                            sc[x][nt][y] = make_float2(softcap_raw(sc[x][nt][y].x, i0, o0), softcap_raw(sc[x][nt][y].y, i1, o1));
-                }
+                    for (int y = 0; y < 2; ++y)
+                        sc[x][y] = make_float2(softcap_raw(sc[x][y].x, i0, o0), softcap_raw(sc[x][y].y, i1, o1));
             }
-            if ((NP > 1 && !two) || tok0 + (NP - 1) * SUB * kPageRows > all_hi || tok0 < all_lo) {
+            if (!two || tok0 + (NP - 1) * SUB * kPageRows > all_hi || tok0 < all_lo) {
 #pragma unroll
                 for (int x = 0; x < NP; ++x)
 #pragma unroll
@@ -1093,14 +1065,12 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
                             for (int g = 0; g < G; ++g) (y ? vm1 : vm0)[x][g] = 0;
                         }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int tok = (nt * 8 + 2 * t4 + e) / a.group;
-                                const int last = a.causal ? L - n + tok : L - 1;
-                                if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
-                                    (e ? sc[x][nt][y].y : sc[x][nt][y].x) = -INFINITY;
-                            }
+                        for (int e = 0; e < 2; ++e) {
+                            const int tok = (row0 + 2 * t4 + e) / a.group;
+                            const int last = a.causal ? L - n + tok : L - 1;
+                            if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
+                                (e ? sc[x][y].y : sc[x][y].x) = -INFINITY;
+                        }
                     }
             }
             // does a score exceed its row's maximum by the slack, or a step the range?
@@ -1110,16 +1080,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
 #pragma unroll
                 for (int g = 0; g < G; ++g) top = max(top, max(vm0[x][g], vm1[x][g]));
             bool over = top >= cap_meta;
-            float2 mx[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
-                if (NP > 1) {
-                    mx[nt].x = fmax3(mx[nt].x, sc[NP - 1][nt][0].x, sc[NP - 1][nt][1].x);
-                    mx[nt].y = fmax3(mx[nt].y, sc[NP - 1][nt][0].y, sc[NP - 1][nt][1].y);
-                }
-                over = over || mx[nt].x > thr[nt].x || mx[nt].y > thr[nt].y;
-            }
+            float2 mx = make_float2(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[0][0].y, sc[0][1].y));
+            mx.x = fmax3(mx.x, sc[1][0].x, sc[1][1].x);
+            mx.y = fmax3(mx.y, sc[1][0].y, sc[1][1].y);
+            over = over || mx.x > thr.x || mx.y > thr.y;
             if (__any_sync(0xffffffffu, over)) {
                 top = __reduce_max_sync(0xffffffffu, top);
                 float resc = 1.0f;
@@ -1133,41 +1097,36 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
                     }
                     cap_meta = (uint32_t)(ex + 128) << 7;
                 }
+                float2 y = mx;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float2 y = mx[nt];
+                for (int o = 4; o < 32; o <<= 1) {
+                    y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
+                    y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
+                }
+                const float2 mn = make_float2(fminf(m.x, -y.x * kf.x), fminf(m.y, -y.y * kf.y));
+                const float2 al = make_float2(ex2(mn.x - m.x), ex2(mn.y - m.y));
+                m = mn;
+                thr.x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf.x;
+                thr.y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf.y;
+                l = fmul2(l, al);
+                const float2 f = make_float2(al.x * resc, al.y * resc);
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
-                        y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
-                    }
-                    const float2 mn = make_float2(fminf(m[nt].x, -y.x * kf[nt].x), fminf(m[nt].y, -y.y * kf[nt].y));
-                    const float2 al = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
-                    m[nt] = mn;
-                    thr[nt].x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf[nt].x;
-                    thr[nt].y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf[nt].y;
-                    l[nt] = fmul2(l[nt], al);
-                    const float2 f = make_float2(al.x * resc, al.y * resc);
+                for (int g = 0; g < G; ++g) zac[g] = fmul2(zac[g], f);
 #pragma unroll
-                    for (int g = 0; g < G; ++g) zac[nt][g] = fmul2(zac[nt][g], f);
-#pragma unroll
-                    for (int c = 0; c < MT; ++c) {
-                        acc[c][nt][0] = fmul2(acc[c][nt][0], f);
-                        acc[c][nt][1] = fmul2(acc[c][nt][1], f);
-                    }
+                for (int c = 0; c < MT; ++c) {
+                    acc[c][0] = fmul2(acc[c][0], f);
+                    acc[c][1] = fmul2(acc[c][1], f);
                 }
             }
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
-                float2 p[NT][2];
+                float2 p[2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float2 d = ffma2(sc[x][nt][y], kf[nt], m[nt]);
-                        p[nt][y] = make_float2(ex2(d.x), ex2(d.y));
-                        l[nt] = fadd2(l[nt], p[nt][y]);
-                    }
+                for (int y = 0; y < 2; ++y) {
+                    const float2 d = ffma2(sc[x][y], kf, m);
+                    p[y] = make_float2(ex2(d.x), ex2(d.y));
+                    l = fadd2(l, p[y]);
+                }
                 uint32_t v0[W], v1[W];
                 load_words<W>(vbase + at[x] * SB, v0);
                 load_words<W>(vbase + at[x] * SB + 128 * W, v1);
@@ -1175,25 +1134,19 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + 4), 1) q4_attn_kernel(con
                 for (int g = 0; g < G; ++g) {
                     const float w0 = q4_step(vm0[x][g]) * beta, w1 = q4_step(vm1[x][g]) * beta;
                     const float z0 = q4_zero(vm0[x][g]), z1 = q4_zero(vm1[x][g]);
-                    uint32_t pb[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float2 x0 = fmul2(p[nt][0], make_float2(w0, w0)), x1 = fmul2(p[nt][1], make_float2(w1, w1));
-                        zac[nt][g] = ffma2(x0, make_float2(z0, z0), ffma2(x1, make_float2(z1, z1), zac[nt][g]));
-                        pb[nt][0] = movmatrix_trans(pack_f16(x0.x, x0.y));
-                        pb[nt][1] = movmatrix_trans(pack_f16(x1.x, x1.y));
-                    }
+                    uint32_t pb[2];
+                    const float2 x0 = fmul2(p[0], make_float2(w0, w0)), x1 = fmul2(p[1], make_float2(w1, w1));
+                    zac[g] = ffma2(x0, make_float2(z0, z0), ffma2(x1, make_float2(z1, z1), zac[g]));
+                    pb[0] = movmatrix_trans(pack_f16(x0.x, x0.y));
+                    pb[1] = movmatrix_trans(pack_f16(x1.x, x1.y));
 #pragma unroll
                     for (int w = g * WG; w < (g + 1) * WG; ++w) {
                         const uint32_t lo[4] = {v0[w] & 0x000f000fu, v0[w] & 0x00f000f0u, v1[w] & 0x000f000fu,
                                                 v1[w] & 0x00f000f0u};
                         const uint32_t y0 = v0[w] >> 8, y1 = v1[w] >> 8;
                         const uint32_t hi[4] = {y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            q4_mma2(acc[2 * w][nt], lo, pb[nt][0], pb[nt][1]);
-                            q4_mma2(acc[2 * w + 1][nt], hi, pb[nt][0], pb[nt][1]);
-                        }
+                        q4_mma2(acc[2 * w], lo, pb[0], pb[1]);
+                        q4_mma2(acc[2 * w + 1], hi, pb[0], pb[1]);
                     }
                 }
             }

@@ -555,7 +555,7 @@ attn_status_t attn_kv_gather_paged_q4(
  *   workspace    >= attn_decode_q4_workspace_size(...) bytes, 16-byte aligned; its
  *                contents on entry do not matter.  Calls that could overlap on the
  *                GPU need one each.
- * Supported: head_dim in {64, 128}, Hq / Hkv <= 16, B <= 4096, any Hkv.
+ * Supported: head_dim in {64, 128}, Hq / Hkv <= 64, B <= 4096, any Hkv.
  */
 size_t attn_decode_q4_workspace_size(int B, int num_heads_q, int num_heads_kv, int head_dim);
 attn_status_t attn_decode_paged_q4(
@@ -573,7 +573,7 @@ attn_status_t attn_decode_paged_q4(
  *   total_k      at least the sum of seqused_k: rows of the workspace (if it is less,
  *                code 531 is reported and the last tokens are left out).
  *   workspace    >= attn_fwd_q4_workspace_size(...) bytes, 16-byte aligned; as above.
- * Up to 16 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
+ * Up to 64 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
  * pages as they are; more, to bf16 rows that the call reads back first.
  */
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int num_heads_q, int num_heads_kv,

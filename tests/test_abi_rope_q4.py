@@ -107,7 +107,7 @@ SCORE_BAD = [(dict(q=None), INVALID), (dict(o=None), INVALID), (dict(used=None),
              (dict(softcap=float("nan")), INVALID), (dict(q=P0 + 8), INVALID), (dict(o=P0 + 2), INVALID)]
 
 
-@pytest.mark.parametrize("kw,want", CACHE_BAD + SCORE_BAD + [(dict(Hq=64), UNSUPPORTED)])
+@pytest.mark.parametrize("kw,want", CACHE_BAD + SCORE_BAD + [(dict(Hq=130), UNSUPPORTED)])
 def test_decode_q4_refusals(L, kw, want):
     base = dict(q=P0, **CACHE, **PAGES, used=P0, B=2, Hq=8, Hkv=2, D=128, group=64, scale=0.0, window=-1, softcap=0.0,
                 o=P0, lse=None, ws=P0, ws_bytes=1 << 30, stream=None)
@@ -127,11 +127,12 @@ def test_fwd_q4_refusals(L, kw, want):
 def test_workspace_sizes(L):
     assert L.attn_decode_q4_workspace_size(0, 8, 2, 128) == 0
     assert L.attn_decode_q4_workspace_size(2, 7, 2, 128) == 0
-    assert L.attn_decode_q4_workspace_size(2, 64, 2, 128) == 0
+    assert L.attn_decode_q4_workspace_size(2, 130, 2, 128) == 0
     small, large = (L.attn_decode_q4_workspace_size(b, 32, 8, 128) for b in (1, 64))
     assert 0 < small < large
-    # past 16 query rows per KV head the packed bf16 rows of K and V
-    assert L.attn_fwd_q4_workspace_size(2, 5, 8, 2, 128, 1000) >= 2 * 1000 * 2 * 128 * 2
+    # past 64 query rows per KV head the packed bf16 rows of K and V
+    assert L.attn_fwd_q4_workspace_size(2, 17, 8, 2, 128, 100000) >= 2 * 100000 * 2 * 128 * 2
+    assert L.attn_fwd_q4_workspace_size(2, 16, 8, 2, 128, 100000) < 2 * 100000 * 2 * 128 * 2
     assert L.attn_fwd_q4_workspace_size(2, -1, 8, 2, 128, 1000) == 0
 
 
