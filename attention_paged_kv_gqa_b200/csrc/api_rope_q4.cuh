@@ -46,41 +46,34 @@ HeadRows head_rows(const void* p, const int64_t* strides) {
     return h;
 }
 
-// Warps that share a token's heads: one, unless that leaves the GPU without
-// enough loads in flight.
+// Warps that share a token's heads: one, unless that leaves an SM with fewer than eight,
+// too few loads in flight.  (1024 tokens of 32 + 8 + 8 heads of 128 into 4-bit pages:
+// 12.3 us with a warp per token, 10.2 at eight warps per SM, 14.3 at sixteen, which repeats
+// the look-up of page and angles too often; 2048: 14.3, 14.3 and 16.4.)
 int rope_parts(long long tokens, int passes, int sms) {
-    const long long want = (long long)sms * 16;
+    const long long want = (long long)sms * 8;
     long long parts = tokens > 0 ? (want + tokens - 1) / tokens : 1;
     return (int)std::max<long long>(1, std::min<long long>(parts, passes));
 }
 
 constexpr int kQ4Smem = 227 * 1024 - 256;      // (some is static)
 
+// Consumer warps of a CTA.  Of one tile of query rows twelve, which hide each other's waits
+// best, though at 128 registers (3 sequences of 65000 keys: 72 us against 75 with eight; 32
+// of 4100 on average: 45 with either).  More tiles repeat a page's scores and weights per
+// tile, and there the eight warps' 168 registers are worth more (16 sequences of 3700 keys,
+// groups of four: 4 queries 47 us against 49, 8 queries 80 against 84, 16 queries 145 against 156).
+int q4_warps(int RT) { return RT == 1 ? 12 : 8; }
+
 // KV heads of a CTA's block, and warps of a head and row tile: the block with the most of
 // the CTA's warps at work, the largest such one (its copies are longest).
 void q4_split(int Hkv, int RT, int* HB, int* SUB) {
+    const int warps = q4_warps(RT);
     int best = 1;
-    for (int hb = 2; hb <= std::min(Hkv, kQ4Warps / RT); ++hb)
-        if (Hkv % hb == 0 && hb * (kQ4Warps / (hb * RT)) >= best * (kQ4Warps / (best * RT))) best = hb;
+    for (int hb = 2; hb <= std::min(Hkv, warps / RT); ++hb)
+        if (Hkv % hb == 0 && hb * (warps / (hb * RT)) >= best * (warps / (best * RT))) best = hb;
     *HB = best;
-    *SUB = kQ4Warps / (best * RT);
-}
-
-// How the partial results of a call are laid out: `slots` of (CTA, sequence and block of
-// heads), each of `parts` for the warps of a head.  A change of sequence is what a CTA's
-// warps can do without meeting (a meeting costs 1.5 us); but where few sequences are
-// spread over many CTAs the combine kernel would read SUB times as many partials (at 148
-// CTAs a sequence 2.5 us against 5), and changes are few.
-struct Q4Parts {
-    size_t slots;
-    int spread, parts;
-};
-Q4Parts q4_parts(int B, int nhb, int SUB, int grid) {
-    Q4Parts p;
-    p.slots = (size_t)grid + (size_t)nhb * B;
-    p.spread = grid / std::max(1, nhb * B);
-    p.parts = p.spread > 8 || p.slots > 2048 ? 1 : SUB;
-    return p;
+    *SUB = warps / (best * RT);
 }
 
 // SMs of the current device; without one more than any has.
@@ -96,40 +89,32 @@ int sm_count_or_most() {
 size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
     int HB, SUB;
     q4_split(Hkv, (rows + 7) / 8, &HB, &SUB);
-    size_t most = 0;                       // (the grid may be smaller than the number of SMs)
-    for (int grid : {sms, std::min(sms, (Hkv / HB) * B * 9)}) {
-        const Q4Parts p = q4_parts(B, Hkv / HB, SUB, grid);
-        most = std::max(most, p.slots * p.parts);
-    }
-    return most * HB * rows * (D + 1) * sizeof(float);
+    // a partial for every (CTA, sequence and block of heads) that meet
+    return ((size_t)sms + (size_t)(Hkv / HB) * B) * HB * rows * (D + 1) * sizeof(float);
 }
 
 bool q4_group_ok(int group_size, int D) {
     return (group_size == 32 || group_size == 64 || group_size == 128) && group_size <= D;
 }
 
-template <int D, int GS>
-attn_status_t launch_q4_rows(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+template <int D, int GS, int WARPS>
+attn_status_t launch_q4_warps(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
     static std::atomic<uint64_t> attr_mask{0};   // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_mask.load() & bit)) {
-        const attn_status_t s = set_smem(q4_attn_kernel<D, GS>, kQ4Smem);
+        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, WARPS>, kQ4Smem);
         if (s != ATTN_OK) return s;
         attr_mask.fetch_or(bit);
     }
-    a.rows = a.max_q * a.group;
-    a.RT = (a.rows + 7) / 8;
     q4_split(a.Hkv, a.RT, &a.HB, &a.SUB);
     const int U = a.HB * a.RT;
     a.nhb = a.Hkv / a.HB;
     const long long bound = (long long)a.B * (a.max_blocks + kQ4Switch) * a.nhb;    // of the cost
     if (bound >= (1LL << 31)) return ATTN_ERR_UNSUPPORTED;
     const int grid = (int)std::min<long long>(sms, bound);
-    const Q4Parts p = q4_parts(a.B, a.nhb, a.SUB, grid);
-    a.parts = p.parts;
-    const size_t rows = p.slots * p.parts * a.HB * a.rows;
+    const size_t rows = ((size_t)grid + (size_t)a.nhb * a.B) * a.HB * a.rows;      // of partials
     if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
     if (workspace_bytes < rows * (D + 1) * sizeof(float))
         return ATTN_ERR_WORKSPACE_TOO_SMALL;
@@ -147,14 +132,23 @@ attn_status_t launch_q4_rows(Q4AttnArgs a, int sms, void* workspace, size_t work
     ns = ns / a.SUB * a.SUB;
     if (ns < 2 * a.SUB) return ATTN_ERR_UNSUPPORTED;
     a.nstages = ns;
-    const int per_row = p.spread * p.parts;
+    const int per_row = grid / (a.nhb * a.B);
     a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;
-    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS>, dim3(grid), dim3(kQ4Threads),
+    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS, WARPS>, dim3(grid), dim3(32 * (WARPS + kQ4Producers)),
                                        C::smem_bytes(a.HB, U, a.SUB, a.B, ns), st, true, a);
     if (s != ATTN_OK) return s;
-    // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp
+    // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp,
+    // whose loads are then all in flight together
     const long long rows_out = (long long)a.B * a.max_q * a.Hq;
     return launch_maybe_pdl(q4_combine_kernel<D>, dim3((unsigned)((rows_out * a.wpr + 7) / 8)), dim3(256), 0, st, true, a);
+}
+
+template <int D, int GS>
+attn_status_t launch_q4_rows(Q4AttnArgs a, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
+    a.rows = a.max_q * a.group;
+    a.RT = (a.rows + 7) / 8;
+    return q4_warps(a.RT) == 12 ? launch_q4_warps<D, GS, 12>(a, sms, ws, ws_bytes, st)
+                                : launch_q4_warps<D, GS, 8>(a, sms, ws, ws_bytes, st);
 }
 
 attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -167,9 +161,12 @@ attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, s
 
 template <int D, int GS>
 attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
-    // a page and head per warp; every block builds the tables, so no more blocks than fill the GPU
+    // A page and head per warp at a time; every block builds the tables, so no more blocks than
+    // two to an SM, which write neighbouring rows closer in time than more do (8 sequences of
+    // 16000 tokens: 132 us, at four to an SM 150, with a block for every eight pages and heads
+    // 131; 512 of 100: 69.6, 69.3 and 94; below 30000 tokens all alike).
     const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv;
-    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 4));
+    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 2));
     q4_gather_kernel<D, GS><<<grid, 256, 2 * (a.B + 1) * sizeof(int), st>>>(a);
     return launch_status();
 }

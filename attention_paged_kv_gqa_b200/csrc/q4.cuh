@@ -465,8 +465,7 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // shows by one vote.
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
 constexpr int kQ4Recentre = 16;          // pages
-constexpr int kQ4Warps = 12;             // consumer warps of a CTA; and producer warps for K, V, their metas, the queries
-constexpr int kQ4Threads = 32 * (kQ4Warps + 4);
+constexpr int kQ4Producers = 4;          // warps that fetch K, V, their metas, the queries
 constexpr int kQ4Tiles = 8;              // row tiles at most
 constexpr int kQ4Switch = 13;            // pages that a change of sequence costs a CTA (for equal shares)
 constexpr float kQ4NoMax = -3.0e38f;     // the maximum before the first key (finite: differences with it stay numbers)
@@ -488,9 +487,8 @@ struct Q4AttnArgs {
     int window;              // < 0: none
     float softcap;           // 0: none
     int rows;                // query rows of a KV head: group * max_q
-    int parts;               // partials of a (CTA, sequence): 1, its warps of a head joined in the CTA, or SUB
-    float* o_part;           // [slots][parts][HB][rows][D]
-    float* lse_part;         // [slots][parts][HB][rows]
+    float* o_part;           // [slots][HB][rows][D]
+    float* lse_part;         // [slots][HB][rows]
     int grid;                // CTAs
     int nstages;
     int wpr;                 // combine: warps of a row (1, 2, 4 or 8)
@@ -622,8 +620,8 @@ __device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int grou
     }
 }
 
-template <int D, int GS>
-__global__ void __launch_bounds__(kQ4Threads, 1) q4_attn_kernel(const Q4AttnArgs a) {
+template <int D, int GS, int WARPS>
+__global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel(const Q4AttnArgs a) {
     using C = Q4Cfg<D, GS>;
     constexpr int W = D / 32;            // words of a lane's K row piece; V words per token pair
     constexpr int G = D / GS;            // groups of a head
@@ -753,9 +751,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_attn_kernel(const Q4AttnArgs
     };
     const Place start = {first_place[0], first_place[1], ends(first_place[0], first_place[1])};
 
-    if (warp >= kQ4Warps) {
+    if (warp >= WARPS) {
         // ------------------------------------------------------------ producers: K, V, metas, queries
-        const int which = warp - kQ4Warps;
+        const int which = warp - WARPS;
         if (which == 3) {
             Place x = start;
             for (int turn = 1; x.end < npages; ++turn) {
@@ -879,7 +877,7 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_attn_kernel(const Q4AttnArgs
         const int slots = (SUB + 1) / 2;
         float2* mine = reinterpret_cast<float2*>(mrg) + unit * slots * 32 * FL;
         int width = 1;
-        while (width < SUB && a.parts == 1) width <<= 1;
+        while (width < SUB) width <<= 1;
         for (int st = width / 2; st > 0; st >>= 1) {
             if (sub >= st && sub < 2 * st) {
                 float2* x = mine + (sub - st) * 32 * FL + lane;
@@ -914,9 +912,9 @@ __global__ void __launch_bounds__(kQ4Threads, 1) q4_attn_kernel(const Q4AttnArgs
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
         }
-        if (sub >= a.parts) return;
+        if (sub > 0) return;
         const float back = 64.0f / beta;             // a power of two, within range for every step
-        const long long base = ((((long long)blockIdx.x + vb) * a.parts + sub) * HB + h) * a.rows;
+        const long long base = (((long long)blockIdx.x + vb) * HB + h) * a.rows;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = row0 + 2 * t4 + e;
@@ -1196,8 +1194,8 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     mine = __reduce_add_sync(0xffffffffu, mine);
     const int share = q4_share(PC, a);
     const int c0 = (hb * PC + cb + kQ4Switch) / share;            // the CTAs of its first and last page
-    const int ns = live && mine > 0 ? ((hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1) * a.parts : 0;
-    const long long first = (((long long)c0 + hb * a.B + b) * a.parts * a.HB + h) * a.rows + row;
+    const int ns = live && mine > 0 ? (hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1 : 0;
+    const long long first = (((long long)c0 + hb * a.B + b) * a.HB + h) * a.rows + row;
     const long long step = (long long)a.HB * a.rows * a.wpr;      // rows between this warp's partials
     float M = -INFINITY, sum = 0.0f, acc[V];
     bool nan = false;
