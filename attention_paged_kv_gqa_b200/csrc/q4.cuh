@@ -28,7 +28,7 @@
 
 namespace attn {
 
-enum : int { kErrQ4Rows = 531, kErrQ4Full = 541, kErrQ4Empty = 542 };
+enum : int { kErrQ4Rows = 531, kErrQ4Queries = 532, kErrQ4Full = 541, kErrQ4Empty = 542 };
 
 // ---------------------------------------------------------------- quantiser
 struct Q4Group {
@@ -550,10 +550,13 @@ __device__ __forceinline__ int q4_first_key(int L, int n, int window) {
     return window >= 0 ? max(0, L - n - window) : 0;
 }
 
-// Pages that sequence b's queries read, of one block of KV heads.
+// Queries of sequence b (those within total_q and max_q).
 __device__ __forceinline__ int q4_queries(const Q4AttnArgs& a, int b) {
-    return a.cu_q ? min(max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0), a.max_q) : 1;
+    if (!a.cu_q) return 1;
+    const int q0 = __ldg(&a.cu_q[b]), q1 = __ldg(&a.cu_q[b + 1]);
+    return q0 < 0 ? 0 : min(max(min(q1, a.total_q) - q0, 0), a.max_q);
 }
+// Pages that they read, of one block of KV heads.
 __device__ __forceinline__ int q4_pages(const Q4AttnArgs& a, int b) {
     const int L = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows), n = q4_queries(a, b);
     return n > 0 ? (L + kPageRows - 1) / kPageRows - q4_first_key(L, n, a.window) / kPageRows : 0;
@@ -614,7 +617,7 @@ __device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int grou
                                          pack_f16(bf16_lo(x[w].y) * up, bf16_lo(x[w].w) * up),
                                          pack_f16(bf16_hi(x[w].y) * up1, bf16_hi(x[w].w) * up1));
     if (t4 == 0) {
-        rows[r8] = down * unit;
+        rows[r8] = fmaxf(down * unit, 1e-33f);       // (with 0 a masked score's minus infinity would give a NaN)
 #pragma unroll
         for (int g = 0; g < G; ++g) rows[(1 + g) * 8 + r8] = -sum[g] / down;
     }
@@ -660,6 +663,8 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
             if (b < a.B) {
                 lenv[b] = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows);
                 cnt = q4_pages(a, b);
+                if (a.cu_q && blockIdx.x == 0 && q4_queries(a, b) != max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0))
+                    record_data_error(kErrQ4Queries);
             }
             int incl = cnt;
 #pragma unroll
@@ -1177,7 +1182,7 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     bool live = w < (long long)a.B * per;
     const int b = live ? (int)(w / per) : 0, tok = live ? (int)(w % per) / a.Hq : 0, hq = live ? (int)(w % per) % a.Hq : 0;
     const long long q0 = a.cu_q ? __ldg(&a.cu_q[b]) : b;
-    if (a.cu_q) live = live && tok < __ldg(&a.cu_q[b + 1]) - q0;
+    live = live && tok < q4_queries(a, b);
     const int hkv = hq / a.group, hb = hkv / a.HB, h = hkv % a.HB;
     const int row = tok * a.group + hq % a.group;
     // The shares follow from the lengths alone: worked out while the attention kernel still

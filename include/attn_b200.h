@@ -117,7 +117,8 @@ const char *attn_status_string(attn_status_t status);
  *     cache, that token not written; 521/522 rotary positions: a position
  *     outside the table, whose nearest row is used / an axis outside the given
  *     ones, axis 0 used; 531 4-bit cache: more rows than the caller's total, the
- *     rest left out).  Nothing else stops on these.
+ *     rest left out; 532: queries past total_q or max_seqlen_q, left out).  Nothing
+ *     else stops on these.
  *   - Neither: ATTN_OK and *code_out = 0.
  */
 attn_status_t attn_device_error(int *code_out, attn_stream_t stream);

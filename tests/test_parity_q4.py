@@ -303,6 +303,19 @@ def test_decode_steps_of_very_different_size():
         check(o, lse, o_ref, lse_ref.T.copy(), tol_o, tol_lse)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_decode_zero_queries_of_a_tiny_scale(softcap):
+    # the smallest unit of a score times the smallest scale is not a float
+    Hq, Hkv, D, group, lens, scale = 4, 2, 64, 32, [37, 5], 1e-25
+    bt, pool = table_for(lens)
+    cache = R.fill((pool, Hkv, 16, D // 2), group, 5)
+    q = randn((2, Hq, D), 6)
+    q[:, ::2] = 0
+    o, lse = A.attn_decode_paged_q4(q.to(DEV), *dev(*cache), bt.to(DEV), i32(lens).to(DEV), scale=scale, softcap=softcap)
+    o_ref, lse_ref = reference(q, cache, bt, lens, i32([0, 1, 2]), scale, True, -1, softcap)
+    check(o, lse, o_ref, lse_ref.T, *tolerances(q, cache, scale))
+
+
 def test_decode_ignores_what_lies_behind_the_length():
     """NaN steps in the last page's free rows and in unused pages change nothing."""
     lens = [5, 18, 0]
@@ -494,6 +507,26 @@ def test_fwd_total_k():
     A.attn_fwd_varlen_paged_q4(q, *cache, block_table=bt.to(DEV), cu_seqlens_q=i32([0, 20, 40]).to(DEV), max_seqlen_q=40,
                                seqused_k=i32(lens).to(DEV), total_k=120, mask=A.MASK_CAUSAL)
     assert A.attn_device_error() == 531
+
+
+def test_fwd_reports_queries_outside():
+    # offsets past total_q, and more queries than max_seqlen_q: reported, the rows inside computed
+    Hq, Hkv, D, group, lens = 4, 2, 64, 32, [40, 70]
+    bt, pool = table_for(lens)
+    cache = R.fill((pool, Hkv, 16, D // 2), group, 5)
+    q = randn((5, Hq, D), 6)
+    run = lambda cu, most: A.attn_fwd_varlen_paged_q4(
+        q.to(DEV), *dev(*cache), block_table=bt.to(DEV), cu_seqlens_q=i32(cu).to(DEV), max_seqlen_q=most,
+        seqused_k=i32(lens).to(DEV), total_k=sum(lens), mask=1)
+    o, lse = run([0, 2, 9], 7)
+    assert A.attn_device_error() == 532
+    o_ref, lse_ref = reference(q, cache, bt, lens, i32([0, 2, 5]), 1 / math.sqrt(D), True, -1, 0.0)
+    check(o, lse, o_ref, lse_ref, *tolerances(q, cache, 1 / math.sqrt(D)))
+    run([0, 2, 5], 2)
+    assert A.attn_device_error() == 532
+    run([-1, 2, 5], 3)
+    assert A.attn_device_error() == 532
+    assert A.attn_device_error() == 0
 
 
 def test_fwd_leaves_rows_behind_the_last_sequence():
