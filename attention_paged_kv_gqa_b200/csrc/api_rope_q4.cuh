@@ -56,24 +56,28 @@ int rope_parts(long long tokens, int passes, int sms) {
     return (int)std::max<long long>(1, std::min<long long>(parts, passes));
 }
 
+constexpr int kQ4Few = 32 * kQ4Scan;
 constexpr int kQ4Smem = 227 * 1024 - 256;      // (some is static)
 
-// Consumer warps of a CTA.  Of one tile of query rows twelve, which hide each other's waits
-// best, though at 128 registers (3 sequences of 65000 keys: 72 us against 75 with eight; 32
-// of 4100 on average: 45 with either).  More tiles repeat a page's scores and weights per
-// tile, and there the eight warps' 168 registers are worth more (16 sequences of 3700 keys,
-// groups of four: 4 queries 47 us against 49, 8 queries 80 against 84, 16 queries 145 against 156).
-int q4_warps(int RT) { return RT == 1 ? 12 : 8; }
+// Eights of query rows that a warp holds.  Up to eight rows: one, which at 128 registers leaves
+// room for twelve warps, and those hide each other's waits best (3 sequences of 65000 keys 72
+// us, with eight warps 75).  More: two, so that half as many warps take the codes of a page
+// apart; they need 168 registers, eight warps (16 sequences of 3700 keys, groups of four: 8
+// queries 70 us, one eight to each of eight warps 81, of twelve 84; 16 queries 119, 148, 156).
+int q4_tile(int rows) { return rows <= 8 ? 1 : 2; }
 
-// KV heads of a CTA's block, and warps of a head and row tile: the block with the most of
-// the CTA's warps at work, the largest such one (its copies are longest).
-void q4_split(int Hkv, int RT, int* HB, int* SUB) {
-    const int warps = q4_warps(RT);
+// Row tiles of a KV head, KV heads of a CTA's block, and warps of a head and row tile: the
+// block with the most of the CTA's warps at work, the largest such one (its copies are
+// longest), but of two eights to a warp at most four heads: with eight, whose queries take
+// twice as long to prepare, 4 queries take 47 us in place of 43 (with two 48).
+void q4_split(int Hkv, int rows, int* RT, int* HB, int* SUB) {
+    const int NT = q4_tile(rows), warps = q4_warps(NT);
+    *RT = (rows + 8 * NT - 1) / (8 * NT);
     int best = 1;
-    for (int hb = 2; hb <= std::min(Hkv, warps / RT); ++hb)
-        if (Hkv % hb == 0 && hb * (warps / (hb * RT)) >= best * (warps / (best * RT))) best = hb;
+    for (int hb = 2; hb <= std::min(Hkv, std::min(NT == 1 ? warps : 4, warps / *RT)); ++hb)
+        if (Hkv % hb == 0 && hb * (warps / (hb * *RT)) >= best * (warps / (best * *RT))) best = hb;
     *HB = best;
-    *SUB = warps / (best * RT);
+    *SUB = warps / (best * *RT);
 }
 
 // SMs of the current device; without one more than any has.
@@ -86,29 +90,35 @@ int sm_count_or_most() {
     return sm_count(dev);
 }
 
+// The combine kernel takes the shares of more than kQ4Few sequences from a table that the
+// attention kernel leaves behind the partials (600 sequences of 100 keys: 109 us without it,
+// 89 with), those of fewer from the lengths, while the attention kernel still runs (32
+// sequences of 4100 keys: 45.2 us, with the table 46.1).
+size_t q4_table_bytes(int B) { return B > kQ4Few ? 8 + (size_t)(B + 1) * sizeof(int2) : 0; }
+
 size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
-    int HB, SUB;
-    q4_split(Hkv, (rows + 7) / 8, &HB, &SUB);
+    int RT, HB, SUB;
+    q4_split(Hkv, rows, &RT, &HB, &SUB);
     // a partial for every (CTA, sequence and block of heads) that meet
-    return ((size_t)sms + (size_t)(Hkv / HB) * B) * HB * rows * (D + 1) * sizeof(float);
+    return ((size_t)sms + (size_t)(Hkv / HB) * B) * HB * rows * (D + 1) * sizeof(float) + q4_table_bytes(B);
 }
 
 bool q4_group_ok(int group_size, int D) {
     return (group_size == 32 || group_size == 64 || group_size == 128) && group_size <= D;
 }
 
-template <int D, int GS, int WARPS>
-attn_status_t launch_q4_warps(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+template <int D, int GS, int NT>
+attn_status_t launch_q4_tiles(Q4AttnArgs a, int sms, void* workspace, size_t workspace_bytes, cudaStream_t st) {
     static std::atomic<uint64_t> attr_mask{0};   // one bit per device
     int dev = 0;
     cudaGetDevice(&dev);
     const uint64_t bit = 1ull << (dev & 63);
     if (!(attr_mask.load() & bit)) {
-        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, WARPS>, kQ4Smem);
+        const attn_status_t s = set_smem(q4_attn_kernel<D, GS, NT>, kQ4Smem);
         if (s != ATTN_OK) return s;
         attr_mask.fetch_or(bit);
     }
-    q4_split(a.Hkv, a.RT, &a.HB, &a.SUB);
+    q4_split(a.Hkv, a.rows, &a.RT, &a.HB, &a.SUB);
     const int U = a.HB * a.RT;
     a.nhb = a.Hkv / a.HB;
     const long long bound = (long long)a.B * (a.max_blocks + kQ4Switch) * a.nhb;    // of the cost
@@ -116,12 +126,13 @@ attn_status_t launch_q4_warps(Q4AttnArgs a, int sms, void* workspace, size_t wor
     const int grid = (int)std::min<long long>(sms, bound);
     const size_t rows = ((size_t)grid + (size_t)a.nhb * a.B) * a.HB * a.rows;      // of partials
     if (!workspace || !aligned16(workspace)) return ATTN_ERR_INVALID_ARG;
-    if (workspace_bytes < rows * (D + 1) * sizeof(float))
+    if (workspace_bytes < rows * (D + 1) * sizeof(float) + q4_table_bytes(a.B))
         return ATTN_ERR_WORKSPACE_TOO_SMALL;
     a.o_part = static_cast<float*>(workspace);
     a.lse_part = a.o_part + rows * D;
+    if (a.B > kQ4Few) a.table = reinterpret_cast<int2*>(a.o_part + (rows * (D + 1) + 1) / 2 * 2);
     a.grid = grid;
-    using C = Q4Cfg<D, GS>;
+    using C = Q4Cfg<D, GS, NT>;
     int ns = 0;
     while (ns < 64 && C::smem_bytes(a.HB, U, a.SUB, a.B, ns + 1) <= kQ4Smem) ++ns;
     // A multiple of SUB: a stage then holds the pages of the same warps in every round, so a warp
@@ -134,7 +145,7 @@ attn_status_t launch_q4_warps(Q4AttnArgs a, int sms, void* workspace, size_t wor
     a.nstages = ns;
     const int per_row = grid / (a.nhb * a.B);
     a.wpr = per_row <= 8 ? 1 : per_row <= 16 ? 2 : per_row <= 32 ? 4 : 8;
-    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS, WARPS>, dim3(grid), dim3(32 * (WARPS + kQ4Producers)),
+    attn_status_t s = launch_maybe_pdl(q4_attn_kernel<D, GS, NT>, dim3(grid), dim3(32 * (q4_warps(NT) + kQ4Producers)),
                                        C::smem_bytes(a.HB, U, a.SUB, a.B, ns), st, true, a);
     if (s != ATTN_OK) return s;
     // a sequence's pages are spread over about grid / (B nhb) CTAs: eight partials to a warp,
@@ -146,9 +157,8 @@ attn_status_t launch_q4_warps(Q4AttnArgs a, int sms, void* workspace, size_t wor
 template <int D, int GS>
 attn_status_t launch_q4_rows(Q4AttnArgs a, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
     a.rows = a.max_q * a.group;
-    a.RT = (a.rows + 7) / 8;
-    return q4_warps(a.RT) == 12 ? launch_q4_warps<D, GS, 12>(a, sms, ws, ws_bytes, st)
-                                : launch_q4_warps<D, GS, 8>(a, sms, ws, ws_bytes, st);
+    return q4_tile(a.rows) == 1 ? launch_q4_tiles<D, GS, 1>(a, sms, ws, ws_bytes, st)
+                                : launch_q4_tiles<D, GS, 2>(a, sms, ws, ws_bytes, st);
 }
 
 attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, size_t ws_bytes, cudaStream_t st) {
@@ -415,7 +425,7 @@ attn_status_t attn_kv_gather_paged_q4(const void* k_cache, const void* v_cache, 
 }
 
 size_t attn_decode_q4_workspace_size(int B, int Hq, int Hkv, int D) {
-    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 8 * kQ4Tiles) return 0;
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || Hq / Hkv > 64) return 0;
     return q4_workspace(B, Hkv, D, Hq / Hkv, sm_count_or_most()) + 16;
 }
 
@@ -430,7 +440,7 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
     if (s != ATTN_OK) return s;
     if ((s = check_score_mods(ATTN_MASK_CAUSAL, window_left, softcap)) != ATTN_OK) return s;
     if (Hq <= 0 || Hq % Hkv) return ATTN_ERR_INVALID_ARG;
-    if (Hq / Hkv > 8 * kQ4Tiles) return ATTN_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 64) return ATTN_ERR_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(o)) return ATTN_ERR_INVALID_ARG;
     int dev = 0;
     if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
@@ -444,6 +454,7 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
     a.q = static_cast<const __nv_bfloat16*>(q);
     a.max_q = 1;
     a.total_q = B;
+    a.total_k = -1;
     a.k_cache = static_cast<const uint8_t*>(k_cache);
     a.v_cache = static_cast<const uint8_t*>(v_cache);
     a.k_meta = static_cast<const uint16_t*>(k_meta);
@@ -461,11 +472,11 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
     return launch_q4(a, D, group_size, sm_count(dev), workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
 }
 
-// The page stream serves up to eight tiles of eight query rows per KV head (16 sequences of
-// 3688 keys on average, groups of four: 104 us with 9 queries and 157 with 16); above that the
-// pages are read back as packed bf16 rows (exact) and the tensor-core forward runs on those
-// (235 us with 17).
-static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= 8 * kQ4Tiles; }
+// The page stream serves up to 128 query rows per KV head; above that the pages are read back
+// as packed bf16 rows (exact) and the tensor-core forward runs on those.  (Groups of four, 16
+// sequences of 3700 keys: 17 to 32 queries 210 to 217 us, read back 228; 2 sequences of 40000:
+// 281 to 286 us, read back 847.)
+static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= kQ4Rows; }
 
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int D, int total_k) {
     if (B <= 0 || max_seqlen_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || D <= 0 || total_k < 0) return 0;
@@ -507,6 +518,7 @@ attn_status_t attn_fwd_varlen_paged_q4(const void* q, const void* k_cache, const
         a.cu_q = cu_seqlens_q;
         a.max_q = max_seqlen_q;
         a.total_q = total_q;
+        a.total_k = total_k;
         a.k_cache = static_cast<const uint8_t*>(k_cache);
         a.v_cache = static_cast<const uint8_t*>(v_cache);
         a.k_meta = static_cast<const uint16_t*>(k_meta);

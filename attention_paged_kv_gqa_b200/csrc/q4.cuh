@@ -466,7 +466,10 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
 constexpr int kQ4Recentre = 16;          // pages
 constexpr int kQ4Producers = 4;          // warps that fetch K, V, their metas, the queries
-constexpr int kQ4Tiles = 8;              // row tiles at most
+constexpr int kQ4Scan = 4;               // sequences that a lane looks up at once
+constexpr int kQ4Rows = 128;             // query rows of a KV head at most
+// A tile is 8 NT rows, NT = 1 where that holds them all, or 2; a CTA has this many consumer warps.
+__host__ __device__ constexpr int q4_warps(int NT) { return NT == 1 ? 12 : 8; }
 constexpr int kQ4Switch = 13;            // pages that a change of sequence costs a CTA (for equal shares)
 constexpr float kQ4NoMax = -3.0e38f;     // the maximum before the first key (finite: differences with it stay numbers)
 
@@ -477,6 +480,7 @@ struct Q4AttnArgs {
     const int* cu_q;         // [B + 1], or null: one query per sequence
     int max_q;               // query tokens a sequence may have (group * max_q <= 8 RT)
     int total_q;
+    int total_k;             // < 0, or what the caller takes the lengths' sum to be at most
     const uint8_t *k_cache, *v_cache;
     const uint16_t *k_meta, *v_meta;
     const int* block_table;
@@ -489,6 +493,7 @@ struct Q4AttnArgs {
     int rows;                // query rows of a KV head: group * max_q
     float* o_part;           // [slots][HB][rows][D]
     float* lse_part;         // [slots][HB][rows]
+    int2* table;             // [B + 1] pages and the cost before each sequence, for the combine kernel; or null
     int grid;                // CTAs
     int nstages;
     int wpr;                 // combine: warps of a row (1, 2, 4 or 8)
@@ -496,20 +501,21 @@ struct Q4AttnArgs {
     float* lse;              // [Hq][total_q], or [B][Hq] (cu_q null); or null
 };
 
-template <int D, int GS>
+template <int D, int GS, int NT>
 struct Q4Cfg {
     static constexpr int TILE = kPageRows * D / 2;              // bytes of a head's K or V tile
     static constexpr int META = kPageRows * (D / GS) * 2;       // bytes of its metas
     __host__ __device__ static constexpr int stage_bytes(int HB) { return 2 * HB * (TILE + META); }
-    static constexpr int PAIRS = D / 16 * 2 + 3;                // a lane exchanges: accumulators, maxima, sums, beta
+    // pairs that a lane exchanges: accumulators, maxima, sums, beta
+    static constexpr int PAIRS = D / 16 * 2 * NT + 2 * NT + 1;
     // (U: heads x row tiles)
     __host__ __device__ static constexpr int merge_bytes(int U, int SUB) {
         return SUB > 1 ? U * ((SUB + 1) / 2) * 32 * PAIRS * 8 : 0;
     }
     // the queries of a segment, twice: the B fragments of Q^T, then per row the units and sums
     static constexpr int QROWS = 1 + D / GS;
-    static constexpr int FRAG = D / 32 * 512;
-    __host__ __device__ static constexpr int query_bytes(int U) { return U * (FRAG + QROWS * 32); }
+    static constexpr int FRAG = NT * (D / 32) * 512, ROWS = QROWS * 32 * NT;
+    __host__ __device__ static constexpr int query_bytes(int U) { return U * (FRAG + ROWS); }
     __host__ __device__ static constexpr int table_bytes(int B) { return ((3 * B + 2) * 4 + 15) / 16 * 16; }
     __host__ __device__ static constexpr int smem_bytes(int HB, int U, int SUB, int B, int ns) {
         return ns * stage_bytes(HB) + 2 * query_bytes(U) + merge_bytes(U, SUB) + table_bytes(B) + (2 * ns + 4) * 8;
@@ -557,8 +563,8 @@ __device__ __forceinline__ int q4_queries(const Q4AttnArgs& a, int b) {
     return q0 < 0 ? 0 : min(max(min(q1, a.total_q) - q0, 0), a.max_q);
 }
 // Pages that they read, of one block of KV heads.
-__device__ __forceinline__ int q4_pages(const Q4AttnArgs& a, int b) {
-    const int L = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows), n = q4_queries(a, b);
+__device__ __forceinline__ int q4_pages(const Q4AttnArgs& a, int b, int len) {
+    const int L = min(max(len, 0), a.max_blocks * kPageRows), n = q4_queries(a, b);
     return n > 0 ? (L + kPageRows - 1) / kPageRows - q4_first_key(L, n, a.window) / kPageRows : 0;
 }
 // The cost of a CTA's share, PC that of all pages of one block of heads: equal ones, of a
@@ -567,75 +573,90 @@ __device__ __forceinline__ int q4_share(int PC, const Q4AttnArgs& a) {
     return max((int)(((uint32_t)(PC * a.nhb) + a.grid - 1) / (uint32_t)a.grid), 2 * a.SUB);   // (below 2^31)
 }
 
-// Eight query rows (row0 ..) of a KV head, for a sequence of n queries: their B fragments
-// (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word in f16 (second nibbles' dims over
-// 16), and per row the unit of its raw scores in log2 units and minus the sums of q over
-// the groups.  Rows past the last query are zero.
-template <int D, int GS>
-__device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int group, float unit, int n, int row0, uint32_t frag_at,
-                                        uint32_t rows_at) {
-    // (q: the first query of the sequence, at the KV head's first query head; offsets in shared memory)
+// The queries of a sequence of n as the consumers want them: `units` (KV head of the block,
+// row tile) of NT times eight rows, of whose eights this warp takes every step-th from `first`
+// on.  Per eight rows the B fragments (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word in
+// f16 (second nibbles' dims over 16), and per row the unit of its raw scores in log2 units and
+// minus the sums of q over the groups.  Rows past the last query are zero.  The loads of N
+// eights are in flight together.
+template <int D, int GS, int NT, int N>
+__device__ __noinline__ void q4_prepare(const __nv_bfloat16* q, int Hq, int group, float unit, int n, int RT, int units, int first,
+                                        int step, uint32_t frag_at, uint32_t rows_at) {
+    // (q: the first query of the sequence, at the block's first query head; offsets in shared memory)
     extern __shared__ __align__(128) uint8_t q4_smem[];
-    uint4* frag = reinterpret_cast<uint4*>(q4_smem + frag_at);
-    float* rows = reinterpret_cast<float*>(q4_smem + rows_at);
+    using C = Q4Cfg<D, GS, NT>;
     const int lane = threadIdx.x & 31;
     constexpr int W = D / 32, G = D / GS, WG = W / G;
-    const int r8 = lane >> 2, t4 = lane & 3, row = row0 + r8, tok = n == 1 ? row >= group : row / group;
-    const bool live = tok < n;
-    const __nv_bfloat16* qr = q + (live ? ((long long)tok * Hq + row - tok * group) * D : 0);
-    uint4 x[W];
+    const int r8 = lane >> 2, t4 = lane & 3;
+    for (int t0 = first; t0 < units * NT; t0 += N * step) {
+        uint4 x[N][W];
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-        x[w] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * w + 8 * t4)) : make_uint4(0, 0, 0, 0);
-    float big = 0.0f, sum[G];
+        for (int i = 0; i < N; ++i) {
+            const int t = t0 + i * step, h = t / (RT * NT), row = t % (RT * NT) * 8 + r8;
+            const int tok = n == 1 ? row >= group : row / group;
+            const bool live = t < units * NT && tok < n;
+            const __nv_bfloat16* qr = q + (live ? ((long long)tok * Hq + h * group + row - tok * group) * D : 0);
 #pragma unroll
-    for (int g = 0; g < G; ++g) sum[g] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        const uint32_t xs[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            big = fmax3(big, fabsf(bf16_lo(xs[e])), fabsf(bf16_hi(xs[e])));
-            sum[w / WG] += bf16_lo(xs[e]) + bf16_hi(xs[e]);
+            for (int w = 0; w < W; ++w)
+                x[i][w] = live ? __ldg(reinterpret_cast<const uint4*>(qr + 32 * w + 8 * t4)) : make_uint4(0, 0, 0, 0);
         }
-    }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
-        sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-    }
-    // the largest q of the row to [2^13, 2^14)
-    const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 115);
-    const float up = __uint_as_float((uint32_t)(127 + 13 - ex) << 23), up1 = up * 0.0625f;
-    const float down = __uint_as_float((uint32_t)(127 + 11 + ex) << 23);    // 2^24 / up
+        for (int i = 0; i < N; ++i) {
+            const int t = t0 + i * step;
+            if (t >= units * NT) break;
+            float big = 0.0f, sum[G];
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-        frag[w * 32 + lane] = make_uint4(pack_f16(bf16_lo(x[w].x) * up, bf16_lo(x[w].z) * up),
-                                         pack_f16(bf16_hi(x[w].x) * up1, bf16_hi(x[w].z) * up1),
-                                         pack_f16(bf16_lo(x[w].y) * up, bf16_lo(x[w].w) * up),
-                                         pack_f16(bf16_hi(x[w].y) * up1, bf16_hi(x[w].w) * up1));
-    if (t4 == 0) {
-        rows[r8] = fmaxf(down * unit, 1e-33f);       // (with 0 a masked score's minus infinity would give a NaN)
+            for (int g = 0; g < G; ++g) sum[g] = 0.0f;
 #pragma unroll
-        for (int g = 0; g < G; ++g) rows[(1 + g) * 8 + r8] = -sum[g] / down;
+            for (int w = 0; w < W; ++w) {
+                const uint32_t xs[4] = {x[i][w].x, x[i][w].y, x[i][w].z, x[i][w].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    big = fmax3(big, fabsf(bf16_lo(xs[e])), fabsf(bf16_hi(xs[e])));
+                    sum[w / WG] += bf16_lo(xs[e]) + bf16_hi(xs[e]);
+                }
+            }
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
+                sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
+            }
+            // the largest q of the row to [2^13, 2^14)
+            const int ex = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 115);
+            const float up = __uint_as_float((uint32_t)(127 + 13 - ex) << 23), up1 = up * 0.0625f;
+            const float down = __uint_as_float((uint32_t)(127 + 11 + ex) << 23);    // 2^24 / up
+            uint4* frag = reinterpret_cast<uint4*>(q4_smem + frag_at + t * (C::FRAG / NT));
+            float* rows = reinterpret_cast<float*>(q4_smem + rows_at + t / NT * C::ROWS + t % NT * 32);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                frag[w * 32 + lane] = make_uint4(pack_f16(bf16_lo(x[i][w].x) * up, bf16_lo(x[i][w].z) * up),
+                                                 pack_f16(bf16_hi(x[i][w].x) * up1, bf16_hi(x[i][w].z) * up1),
+                                                 pack_f16(bf16_lo(x[i][w].y) * up, bf16_lo(x[i][w].w) * up),
+                                                 pack_f16(bf16_hi(x[i][w].y) * up1, bf16_hi(x[i][w].w) * up1));
+            if (t4 == 0) {
+                rows[r8] = fmaxf(down * unit, 1e-33f);   // (with 0 a masked score's minus infinity would give a NaN)
+#pragma unroll
+                for (int g = 0; g < G; ++g) rows[(1 + g) * 8 * NT + r8] = -sum[g] / down;
+            }
+        }
     }
 }
 
-template <int D, int GS, int WARPS>
-__global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel(const Q4AttnArgs a) {
-    using C = Q4Cfg<D, GS>;
+template <int D, int GS, int NT>
+__global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn_kernel(const Q4AttnArgs a) {
+    using C = Q4Cfg<D, GS, NT>;
     constexpr int W = D / 32;            // words of a lane's K row piece; V words per token pair
     constexpr int G = D / GS;            // groups of a head
     constexpr int WG = W / G;            // words of a group
     constexpr int MT = D / 16;           // 16-column output tiles
-    constexpr int NP = 2;                // pages a warp takes at once: two chains of dependent operations side by side
+    constexpr int NP = NT == 1 ? 2 : 1;  // pages a warp takes at once: two chains of dependent operations side by side
     const int NS = a.nstages, HB = a.HB, SUB = a.SUB, U = HB * a.RT, SB = C::stage_bytes(HB);
     extern __shared__ __align__(128) uint8_t q4_smem[];
     uint8_t* smem = q4_smem;
     uint8_t* tail = smem + NS * SB;
-    uint8_t* qarea = tail;                           // two of: [U][W][32] uint4, [U][QROWS][8] float
+    uint8_t* qarea = tail;                           // two of: [U][NT][W][32] uint4, [U][QROWS][8 NT] float
     const int QB = C::query_bytes(U);
     tail += 2 * QB;
     float* mrg = reinterpret_cast<float*>(tail);
@@ -657,32 +678,51 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     auto queries = [&](int b) { return q4_queries(a, b); };
     if (warp == 0) {
         int run = 0, with_any = 0;
-        for (int base = 0; base < a.B; base += 32) {
-            const int b = base + lane;
-            int cnt = 0;
-            if (b < a.B) {
-                lenv[b] = min(max(a.seqused_k[b], 0), a.max_blocks * kPageRows);
-                cnt = q4_pages(a, b);
-                if (a.cu_q && blockIdx.x == 0 && q4_queries(a, b) != max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0))
-                    record_data_error(kErrQ4Queries);
-            }
-            int incl = cnt;
+        long long keys = 0;
+        for (int base = 0; base < a.B; base += 32 * kQ4Scan) {
+            int cnts[kQ4Scan];
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
+            for (int i = 0; i < kQ4Scan; ++i) {
+                const int b = base + 32 * i + lane;
+                cnts[i] = 0;
+                if (b < a.B) {
+                    const int len = a.seqused_k[b];
+                    lenv[b] = min(max(len, 0), a.max_blocks * kPageRows);
+                    keys += max(len, 0);
+                    cnts[i] = q4_pages(a, b, len);
+                    if (a.cu_q && blockIdx.x == 0 && q4_queries(a, b) != max(__ldg(&a.cu_q[b + 1]) - __ldg(&a.cu_q[b]), 0))
+                        record_data_error(kErrQ4Queries);
+                }
             }
-            const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0);
-            if (b < a.B) {
-                prefix[b] = run + incl - cnt;
-                cost[b] = run + incl - cnt + kQ4Switch * (with_any + __popc(any & ((1u << lane) - 1u)));
+#pragma unroll
+            for (int i = 0; i < kQ4Scan; ++i) {
+                if (base + 32 * i >= a.B) break;
+                const int b = base + 32 * i + lane, cnt = cnts[i];
+                int incl = cnt;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += v;
+                }
+                const uint32_t any = __ballot_sync(0xffffffffu, cnt > 0);
+                if (b < a.B) {
+                    prefix[b] = run + incl - cnt;
+                    cost[b] = run + incl - cnt + kQ4Switch * (with_any + __popc(any & ((1u << lane) - 1u)));
+                    if (a.table && blockIdx.x == 0) a.table[b] = make_int2(cnt, cost[b]);
+                }
+                run += __shfl_sync(0xffffffffu, incl, 31);
+                with_any += __popc(any);
             }
-            run += __shfl_sync(0xffffffffu, incl, 31);
-            with_any += __popc(any);
+        }
+        if (a.total_k >= 0 && blockIdx.x == 0) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) keys += __shfl_xor_sync(0xffffffffu, keys, o);
+            if (keys > a.total_k) record_data_error(kErrQ4Rows);
         }
         if (lane == 0) {
             prefix[a.B] = run;
             cost[a.B] = run + kQ4Switch * with_any;
+            if (a.table && blockIdx.x == 0) a.table[a.B] = make_int2(0, cost[a.B]);
         }
         __syncwarp();
         // The pages of one head block after another, each sequence's behind kQ4Switch units for
@@ -731,13 +771,10 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     // The queries of the share's sequences as the consumers want them, in two areas by turns:
     // the first sequence's by the consumers themselves, the others one sequence ahead by the
     // fourth producer warp.
-    auto prepare = [&](int turn, int hb, int b, int first, int step) {
+    auto prepare = [&](int turn, int hb, int b, int first, int step, auto at_once) {
         const uint32_t to = (uint32_t)(qarea - smem) + (turn & 1) * QB;
         const __nv_bfloat16* q = a.q + ((long long)(a.cu_q ? __ldg(&a.cu_q[b]) : b) * a.Hq + hb * HB * a.group) * D;
-        const int n = queries(b);
-        for (int t = first; t < U; t += step)
-            q4_prepare<D, GS>(q + t / a.RT * a.group * D, a.Hq, a.group, a.scale * kLog2e, n, t % a.RT * 8, to + t * C::FRAG,
-                              to + U * C::FRAG + t * C::QROWS * 32);
+        q4_prepare<D, GS, NT, decltype(at_once)::value>(q, a.Hq, a.group, a.scale * kLog2e, queries(b), a.RT, U, first, step, to, to + U * C::FRAG);
     };
     // The sequences of the share in order: (block of heads, sequence), and the page at which each ends.
     struct Place {
@@ -756,16 +793,16 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     };
     const Place start = {first_place[0], first_place[1], ends(first_place[0], first_place[1])};
 
-    if (warp >= WARPS) {
+    if (warp >= q4_warps(NT)) {
         // ------------------------------------------------------------ producers: K, V, metas, queries
-        const int which = warp - WARPS;
+        const int which = warp - q4_warps(NT);
         if (which == 3) {
             Place x = start;
             for (int turn = 1; x.end < npages; ++turn) {
                 x = next_place(x);
                 bool ok = mbar_wait(&qempty[turn & 1], (turn >> 1 & 1) ^ 1, kErrQ4Empty);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                prepare(turn, x.hb, x.b, 0, 1);
+                prepare(turn, x.hb, x.b, 0, 1, std::integral_constant<int, 2>());
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&qfull[turn & 1]);
             }
@@ -822,31 +859,36 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     if (warp >= U * SUB) return;
     // ---------------------------------------------------------------- consumers
     const int unit = warp / SUB, sub = warp % SUB;   // head and row tile, this warp's share of their pages
-    const int h = unit / a.RT, row0 = unit % a.RT * 8;
+    const int h = unit / a.RT, row0 = unit % a.RT * 8 * NT;
     const int r8 = lane >> 2, t4 = lane & 3;
     const bool capped = a.softcap > 0.0f;
     // this lane's B fragments of Q^T, (dims e = 0, 4), (1, 5), (2, 6), (3, 7) of each word: in
     // shared memory, which spares registers
     uint32_t qb = 0;                     // (its offset in shared memory)
     // of the columns 2 t4 and 2 t4 + 1 (x, y) of each 8-row tile:
-    float2 qs[G];                    // minus the sum of q over a group, in units of the raw score
-    float2 kf;                       // score in log2 units = raw score * kf
-    float2 acc[MT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
-    float2 zac[G];                   // sum w zero, this lane's keys
-    float2 m, l;                 // minus the maximum (log2 units); sum, this lane's keys
-    float2 thr;                      // the raw score that moves the maximum
+    float2 qs[NT][G];                    // minus the sum of q over a group, in units of the raw score
+    float2 kf[NT];                       // score in log2 units = raw score * kf
+    float2 acc[MT][NT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
+    float2 zac[NT][G];                   // sum w zero, this lane's keys
+    float2 m[NT], l[NT];                 // minus the maximum (log2 units); sum, this lane's keys
+    float2 thr[NT];                      // the raw score that moves the maximum
     float beta = 1.0f;                   // w = p step beta
     uint32_t cap_meta = 0;               // metas below it have steps that beta keeps in range
     int since = 0;
     auto reset = [&]() {
         const float2 zero2 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int c = 0; c < MT; ++c) acc[c][0] = acc[c][1] = zero2;
-        m = make_float2(-kQ4NoMax, -kQ4NoMax);
-        thr = make_float2(-INFINITY, -INFINITY);
-        l = zero2;
+        for (int c = 0; c < MT; ++c)
 #pragma unroll
-        for (int g = 0; g < G; ++g) zac[g] = zero2;
+            for (int nt = 0; nt < NT; ++nt) acc[c][nt][0] = acc[c][nt][1] = zero2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = make_float2(-kQ4NoMax, -kQ4NoMax);
+            thr[nt] = make_float2(-INFINITY, -INFINITY);
+            l[nt] = zero2;
+#pragma unroll
+            for (int g = 0; g < G; ++g) zac[nt][g] = zero2;
+        }
         beta = 1.0f;
         cap_meta = 16;                               // a step above zero
         since = 0;
@@ -862,22 +904,25 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     // takes sum w zero out of the accumulators
     auto recentre = [&]() {
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float2 z = over_rows(zac[g]);
-            zac[g] = make_float2(0.0f, 0.0f);
-            const float lo = -5.9604644775390625e-8f, hi = -9.5367431640625e-7f;     // -2^-24, -2^-20
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
-                acc[c][0] = ffma2(z, make_float2(lo, lo), acc[c][0]);
-                acc[c][1] = ffma2(z, make_float2(hi, hi), acc[c][1]);
+            for (int g = 0; g < G; ++g) {
+                const float2 z = over_rows(zac[nt][g]);
+                zac[nt][g] = make_float2(0.0f, 0.0f);
+                const float lo = -5.9604644775390625e-8f, hi = -9.5367431640625e-7f;     // -2^-24, -2^-20
+#pragma unroll
+                for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
+                    acc[c][nt][0] = ffma2(z, make_float2(lo, lo), acc[c][nt][0]);
+                    acc[c][nt][1] = ffma2(z, make_float2(hi, hi), acc[c][nt][1]);
+                }
             }
-        }
         since = 0;
     };
     // the end of a sequence or of the share: join the SUB warps of the head, write the partial
     auto flush_partial = [&](int vb, int n) {
         recentre();
-        l = over_rows(l);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) l[nt] = over_rows(l[nt]);
         constexpr int FL = C::PAIRS;                 // pairs a lane exchanges
         const int slots = (SUB + 1) / 2;
         float2* mine = reinterpret_cast<float2*>(mrg) + unit * slots * 32 * FL;
@@ -887,33 +932,41 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
             if (sub >= st && sub < 2 * st) {
                 float2* x = mine + (sub - st) * 32 * FL + lane;
 #pragma unroll
-                for (int c = 0; c < MT; ++c) {
-                    x[32 * (2 * c)] = acc[c][0];
-                    x[32 * (2 * c + 1)] = acc[c][1];
+                for (int c = 0; c < MT; ++c)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        x[32 * (c * NT + nt) * 2] = acc[c][nt][0];
+                        x[32 * ((c * NT + nt) * 2 + 1)] = acc[c][nt][1];
+                    }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    x[32 * (MT * NT + nt) * 2] = m[nt];
+                    x[32 * ((MT * NT + nt) * 2 + 1)] = l[nt];
                 }
-                x[32 * (2 * MT)] = m;
-                x[32 * (2 * MT + 1)] = l;
-                x[32 * (2 * MT + 2)] = make_float2(beta, 0.0f);
+                x[32 * (FL - 1)] = make_float2(beta, 0.0f);
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
             if (sub < st && sub + st < SUB) {
                 const float2* x = mine + sub * 32 * FL + lane;
-                const float beta2 = x[32 * (2 * MT + 2)].x, nb = fminf(beta, beta2);     // the larger steps' unit
+                const float beta2 = x[32 * (FL - 1)].x, nb = fminf(beta, beta2);     // the larger steps' unit
                 const float r1 = nb / beta, r2 = nb / beta2;
                 beta = nb;
-                const float2 m2 = x[32 * (2 * MT)], l2 = x[32 * (2 * MT + 1)];
-                const float2 mn = make_float2(fminf(m.x, m2.x), fminf(m.y, m2.y));
-                float2 f1 = make_float2(ex2(mn.x - m.x), ex2(mn.y - m.y));
-                float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
-                m = mn;
-                l = ffma2(l, f1, fmul2(l2, f2));
-                f1 = fmul2(f1, make_float2(r1, r1));
-                f2 = fmul2(f2, make_float2(r2, r2));
 #pragma unroll
-                for (int c = 0; c < MT; ++c)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 m2 = x[32 * (MT * NT + nt) * 2], l2 = x[32 * ((MT * NT + nt) * 2 + 1)];
+                    const float2 mn = make_float2(fminf(m[nt].x, m2.x), fminf(m[nt].y, m2.y));
+                    float2 f1 = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
+                    float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
+                    m[nt] = mn;
+                    l[nt] = ffma2(l[nt], f1, fmul2(l2, f2));
+                    f1 = fmul2(f1, make_float2(r1, r1));
+                    f2 = fmul2(f2, make_float2(r2, r2));
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        acc[c][y] = ffma2(acc[c][y], f1, fmul2(x[32 * (2 * c + y)], f2));
+                    for (int c = 0; c < MT; ++c)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            acc[c][nt][y] = ffma2(acc[c][nt][y], f1, fmul2(x[32 * ((c * NT + nt) * 2 + y)], f2));
+                }
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
         }
@@ -921,21 +974,23 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
         const float back = 64.0f / beta;             // a power of two, within range for every step
         const long long base = (((long long)blockIdx.x + vb) * HB + h) * a.rows;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = row0 + 2 * t4 + e;
-            if (row >= n * a.group) continue;
-            const float s = e ? l.y : l.x;
-            const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
-            const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
-            float* rp = a.o_part + (base + row) * D;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int c = 0; c < MT; ++c) {
-                rp[16 * c + r8] = (e ? acc[c][0].y : acc[c][0].x) * lo * back;
-                rp[16 * c + 8 + r8] = (e ? acc[c][1].y : acc[c][1].x) * hi * back;
+            for (int e = 0; e < 2; ++e) {
+                const int row = row0 + nt * 8 + 2 * t4 + e;
+                if (row >= n * a.group) continue;
+                const float s = e ? l[nt].y : l[nt].x;
+                const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
+                const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
+                float* rp = a.o_part + (base + row) * D;
+#pragma unroll
+                for (int c = 0; c < MT; ++c) {
+                    rp[16 * c + r8] = (e ? acc[c][nt][0].y : acc[c][nt][0].x) * lo * back;
+                    rp[16 * c + 8 + r8] = (e ? acc[c][nt][1].y : acc[c][nt][1].x) * hi * back;
+                }
+                if (r8 == 0)
+                    a.lse_part[base + row] = s > 0.0f ? (log2f(s) - (e ? m[nt].y : m[nt].x)) * kLn2 : s == s ? -INFINITY : s;
             }
-            if (r8 == 0)
-                a.lse_part[base + row] = s > 0.0f ? (log2f(s) - (e ? m.y : m.x)) * kLn2 : s == s ? -INFINITY : s;
-        }
     };
     bool ok = true;
     int i = sub, st = sub;                           // this warp's next page of the share, and its stage
@@ -948,7 +1003,7 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
     const uint8_t* vbase = smem + (HB + h) * C::TILE + lane * W * 4;
     const uint8_t* mbase = smem + 2 * HB * C::TILE + h * C::META + r8 * G * 2;
     // raw scores of a page's keys r8 and r8 + 8 against the tile's columns
-    auto scores = [&](int so, float2 (&sc)[2]) {
+    auto scores = [&](int so, float2 (&sc)[NT][2]) {
         uint32_t k0[W], k1[W], km0[G], km1[G];
         load_words<W>(kbase + so, k0);
         load_words<W>(kbase + so + 4 * D, k1);
@@ -956,33 +1011,39 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
         load_metas<G>(mbase + so + 16 * G, km1);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            float raw[4], raw2[4];
+            float raw[NT][4], raw2[NT][4];
 #pragma unroll
             for (int w = g * WG; w < (g + 1) * WG; ++w) {
                 const uint32_t lo[4] = {k0[w] & 0x000f000fu, k1[w] & 0x000f000fu, k0[w] & 0x00f000f0u, k1[w] & 0x00f000f0u};
                 const uint32_t x0 = k0[w] >> 8, x1 = k1[w] >> 8;
                 const uint32_t hi[4] = {x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u};
-                const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + w * 512);
-                if (WG == 1) {
-                    q4_mma_first(raw, lo, qw.x, qw.y);
-                    q4_mma(raw, hi, qw.z, qw.w);
-                } else if (w == g * WG) {
-                    q4_mma_first(raw, lo, qw.x, qw.y);
-                    q4_mma_first(raw2, hi, qw.z, qw.w);
-                } else {
-                    q4_mma(raw, lo, qw.x, qw.y);
-                    q4_mma(raw2, hi, qw.z, qw.w);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint4 qw = *reinterpret_cast<const uint4*>(smem + qb + (nt * W + w) * 512);
+                    if (WG == 1) {
+                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
+                        q4_mma(raw[nt], hi, qw.z, qw.w);
+                    } else if (w == g * WG) {
+                        q4_mma_first(raw[nt], lo, qw.x, qw.y);
+                        q4_mma_first(raw2[nt], hi, qw.z, qw.w);
+                    } else {
+                        q4_mma(raw[nt], lo, qw.x, qw.y);
+                        q4_mma(raw2[nt], hi, qw.z, qw.w);
+                    }
                 }
             }
             const float s0 = q4_step(km0[g]), s1 = q4_step(km1[g]), z0 = q4_zero(km0[g]), z1 = q4_zero(km1[g]);
-            float2 d0 = make_float2(raw[0], raw[1]), d1 = make_float2(raw[2], raw[3]);
-            if (WG > 1) {
-                d0 = fadd2(d0, make_float2(raw2[0], raw2[1]));
-                d1 = fadd2(d1, make_float2(raw2[2], raw2[3]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float2 d0 = make_float2(raw[nt][0], raw[nt][1]), d1 = make_float2(raw[nt][2], raw[nt][3]);
+                if (WG > 1) {
+                    d0 = fadd2(d0, make_float2(raw2[nt][0], raw2[nt][1]));
+                    d1 = fadd2(d1, make_float2(raw2[nt][2], raw2[nt][3]));
+                }
+                const float2 y0 = ffma2(make_float2(z0, z0), qs[nt][g], d0), y1 = ffma2(make_float2(z1, z1), qs[nt][g], d1);
+                sc[nt][0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[nt][0]);
+                sc[nt][1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[nt][1]);
             }
-            const float2 y0 = ffma2(make_float2(z0, z0), qs[g], d0), y1 = ffma2(make_float2(z1, z1), qs[g], d1);
-            sc[0] = g == 0 ? fmul2(y0, make_float2(s0, s0)) : ffma2(y0, make_float2(s0, s0), sc[0]);
-            sc[1] = g == 0 ? fmul2(y1, make_float2(s1, s1)) : ffma2(y1, make_float2(s1, s1), sc[1]);
         }
     };
     int turn = 0;                                    // sequences of the share so far
@@ -995,7 +1056,7 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
         const int key0 = (g0 - prefix[b] + q4_first_key(L, n, a.window) / kPageRows) * kPageRows;
         reset();
         if (turn == 0) {
-            prepare(0, hb, b, warp, U * SUB);
+            prepare(0, hb, b, warp, U * SUB, std::integral_constant<int, 1>());
             asm volatile("bar.sync 15, %0;" ::"r"(32 * U * SUB) : "memory");
         } else if (ok) {
             ok = mbar_wait(&qfull[turn & 1], (turn >> 1 & 1) ^ (turn & 1 ^ 1), kErrQ4Full);
@@ -1004,17 +1065,20 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
         {
             const uint8_t* q = qarea + (turn & 1) * QB;
             qb = (uint32_t)(qarea - smem) + (turn & 1) * QB + unit * C::FRAG + lane * 16;
-            const float* rows = reinterpret_cast<const float*>(q + U * C::FRAG) + unit * C::QROWS * 8 + 2 * t4;
-            kf = *reinterpret_cast<const float2*>(rows);
+            const float* rows = reinterpret_cast<const float*>(q + U * C::FRAG + unit * C::ROWS) + 2 * t4;
 #pragma unroll
-            for (int g = 0; g < G; ++g) qs[g] = *reinterpret_cast<const float2*>(rows + (1 + g) * 8);
+            for (int nt = 0; nt < NT; ++nt) {
+                kf[nt] = *reinterpret_cast<const float2*>(rows + 8 * nt);
+#pragma unroll
+                for (int g = 0; g < G; ++g) qs[nt][g] = *reinterpret_cast<const float2*>(rows + (1 + g) * 8 * NT + 8 * nt);
+            }
         }
         // pages whose keys every query sees: key0 of the page in [all_lo, all_hi]
         const int all_hi = (a.causal ? L - n : L - 1) - (kPageRows - 1);
         const int all_lo = a.window >= 0 ? L - 1 - a.window : 0;
         // waits for this warp's next page (and the one after); their stages go to `at`
         auto take = [&](int (&at)[NP]) {
-            const bool two = i + SUB < seg_end;
+            const bool two = NP > 1 && i + SUB < seg_end;
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
                 if (x == 0 || two) {
@@ -1036,7 +1100,7 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
             return two;
         };
         int at[NP];
-        float2 sc[NP][2];
+        float2 sc[NP][NT][2];
         while (i < seg_end) {
             const int tok0 = key0 + (i - seg) * kPageRows;
             const bool two = take(at);
@@ -1049,15 +1113,18 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
                 load_metas<G>(mbase + at[x] * SB + HB * C::META + 16 * G, vm1[x]);
             }
             if (capped) {
-                const float b0 = kf.x * kLn2, b1 = kf.y * kLn2;             // to natural units
-                const float i0 = b0 / a.softcap, i1 = b1 / a.softcap, o0 = a.softcap / b0, o1 = a.softcap / b1;
 #pragma unroll
-                for (int x = 0; x < NP; ++x)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float b0 = kf[nt].x * kLn2, b1 = kf[nt].y * kLn2;             // to natural units
+                    const float i0 = b0 / a.softcap, i1 = b1 / a.softcap, o0 = a.softcap / b0, o1 = a.softcap / b1;
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        sc[x][y] = make_float2(softcap_raw(sc[x][y].x, i0, o0), softcap_raw(sc[x][y].y, i1, o1));
+                    for (int x = 0; x < NP; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            sc[x][nt][y] = make_float2(softcap_raw(sc[x][nt][y].x, i0, o0), softcap_raw(sc[x][nt][y].y, i1, o1));
+                }
             }
-            if (!two || tok0 + (NP - 1) * SUB * kPageRows > all_hi || tok0 < all_lo) {
+            if ((NP > 1 && !two) || tok0 + (NP - 1) * SUB * kPageRows > all_hi || tok0 < all_lo) {
 #pragma unroll
                 for (int x = 0; x < NP; ++x)
 #pragma unroll
@@ -1068,12 +1135,14 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
                             for (int g = 0; g < G; ++g) (y ? vm1 : vm0)[x][g] = 0;
                         }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int tok = (row0 + 2 * t4 + e) / a.group;
-                            const int last = a.causal ? L - n + tok : L - 1;
-                            if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
-                                (e ? sc[x][y].y : sc[x][y].x) = -INFINITY;
-                        }
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int tok = (row0 + nt * 8 + 2 * t4 + e) / a.group;
+                                const int last = a.causal ? L - n + tok : L - 1;
+                                if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
+                                    (e ? sc[x][nt][y].y : sc[x][nt][y].x) = -INFINITY;
+                            }
                     }
             }
             // does a score exceed its row's maximum by the slack, or a step the range?
@@ -1083,10 +1152,16 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
 #pragma unroll
                 for (int g = 0; g < G; ++g) top = max(top, max(vm0[x][g], vm1[x][g]));
             bool over = top >= cap_meta;
-            float2 mx = make_float2(fmaxf(sc[0][0].x, sc[0][1].x), fmaxf(sc[0][0].y, sc[0][1].y));
-            mx.x = fmax3(mx.x, sc[1][0].x, sc[1][1].x);
-            mx.y = fmax3(mx.y, sc[1][0].y, sc[1][1].y);
-            over = over || mx.x > thr.x || mx.y > thr.y;
+            float2 mx[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                mx[nt] = make_float2(fmaxf(sc[0][nt][0].x, sc[0][nt][1].x), fmaxf(sc[0][nt][0].y, sc[0][nt][1].y));
+                if (NP > 1) {
+                    mx[nt].x = fmax3(mx[nt].x, sc[NP - 1][nt][0].x, sc[NP - 1][nt][1].x);
+                    mx[nt].y = fmax3(mx[nt].y, sc[NP - 1][nt][0].y, sc[NP - 1][nt][1].y);
+                }
+                over = over || mx[nt].x > thr[nt].x || mx[nt].y > thr[nt].y;
+            }
             if (__any_sync(0xffffffffu, over)) {
                 top = __reduce_max_sync(0xffffffffu, top);
                 float resc = 1.0f;
@@ -1100,36 +1175,41 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
                     }
                     cap_meta = (uint32_t)(ex + 128) << 7;
                 }
-                float2 y = mx;
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) {
-                    y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
-                    y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
-                }
-                const float2 mn = make_float2(fminf(m.x, -y.x * kf.x), fminf(m.y, -y.y * kf.y));
-                const float2 al = make_float2(ex2(mn.x - m.x), ex2(mn.y - m.y));
-                m = mn;
-                thr.x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf.x;
-                thr.y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf.y;
-                l = fmul2(l, al);
-                const float2 f = make_float2(al.x * resc, al.y * resc);
+                for (int nt = 0; nt < NT; ++nt) {
+                    float2 y = mx[nt];
 #pragma unroll
-                for (int g = 0; g < G; ++g) zac[g] = fmul2(zac[g], f);
+                    for (int o = 4; o < 32; o <<= 1) {
+                        y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
+                        y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
+                    }
+                    const float2 mn = make_float2(fminf(m[nt].x, -y.x * kf[nt].x), fminf(m[nt].y, -y.y * kf[nt].y));
+                    const float2 al = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
+                    m[nt] = mn;
+                    thr[nt].x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf[nt].x;
+                    thr[nt].y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf[nt].y;
+                    l[nt] = fmul2(l[nt], al);
+                    const float2 f = make_float2(al.x * resc, al.y * resc);
 #pragma unroll
-                for (int c = 0; c < MT; ++c) {
-                    acc[c][0] = fmul2(acc[c][0], f);
-                    acc[c][1] = fmul2(acc[c][1], f);
+                    for (int g = 0; g < G; ++g) zac[nt][g] = fmul2(zac[nt][g], f);
+#pragma unroll
+                    for (int c = 0; c < MT; ++c) {
+                        acc[c][nt][0] = fmul2(acc[c][nt][0], f);
+                        acc[c][nt][1] = fmul2(acc[c][nt][1], f);
+                    }
                 }
             }
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
-                float2 p[2];
+                float2 p[NT][2];
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float2 d = ffma2(sc[x][y], kf, m);
-                    p[y] = make_float2(ex2(d.x), ex2(d.y));
-                    l = fadd2(l, p[y]);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float2 d = ffma2(sc[x][nt][y], kf[nt], m[nt]);
+                        p[nt][y] = make_float2(ex2(d.x), ex2(d.y));
+                        l[nt] = fadd2(l[nt], p[nt][y]);
+                    }
                 uint32_t v0[W], v1[W];
                 load_words<W>(vbase + at[x] * SB, v0);
                 load_words<W>(vbase + at[x] * SB + 128 * W, v1);
@@ -1137,19 +1217,25 @@ __global__ void __launch_bounds__(32 * (WARPS + kQ4Producers), 1) q4_attn_kernel
                 for (int g = 0; g < G; ++g) {
                     const float w0 = q4_step(vm0[x][g]) * beta, w1 = q4_step(vm1[x][g]) * beta;
                     const float z0 = q4_zero(vm0[x][g]), z1 = q4_zero(vm1[x][g]);
-                    uint32_t pb[2];
-                    const float2 x0 = fmul2(p[0], make_float2(w0, w0)), x1 = fmul2(p[1], make_float2(w1, w1));
-                    zac[g] = ffma2(x0, make_float2(z0, z0), ffma2(x1, make_float2(z1, z1), zac[g]));
-                    pb[0] = movmatrix_trans(pack_f16(x0.x, x0.y));
-                    pb[1] = movmatrix_trans(pack_f16(x1.x, x1.y));
+                    uint32_t pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float2 x0 = fmul2(p[nt][0], make_float2(w0, w0)), x1 = fmul2(p[nt][1], make_float2(w1, w1));
+                        zac[nt][g] = ffma2(x0, make_float2(z0, z0), ffma2(x1, make_float2(z1, z1), zac[nt][g]));
+                        pb[nt][0] = movmatrix_trans(pack_f16(x0.x, x0.y));
+                        pb[nt][1] = movmatrix_trans(pack_f16(x1.x, x1.y));
+                    }
 #pragma unroll
                     for (int w = g * WG; w < (g + 1) * WG; ++w) {
                         const uint32_t lo[4] = {v0[w] & 0x000f000fu, v0[w] & 0x00f000f0u, v1[w] & 0x000f000fu,
                                                 v1[w] & 0x00f000f0u};
                         const uint32_t y0 = v0[w] >> 8, y1 = v1[w] >> 8;
                         const uint32_t hi[4] = {y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u};
-                        q4_mma2(acc[2 * w], lo, pb[0], pb[1]);
-                        q4_mma2(acc[2 * w + 1], hi, pb[0], pb[1]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            q4_mma2(acc[2 * w][nt], lo, pb[nt][0], pb[nt][1]);
+                            q4_mma2(acc[2 * w + 1][nt], hi, pb[nt][0], pb[nt][1]);
+                        }
                     }
                 }
             }
@@ -1185,28 +1271,47 @@ __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     live = live && tok < q4_queries(a, b);
     const int hkv = hq / a.group, hb = hkv / a.HB, h = hkv % a.HB;
     const int row = tok * a.group + hq % a.group;
-    // The shares follow from the lengths alone: worked out while the attention kernel still
-    // runs (which began after whatever wrote the lengths had ended).
+    // The shares follow from the lengths alone: few are worked out while the attention kernel
+    // still runs (which began after whatever wrote the lengths had ended), many taken from it.
     int PC = 0, cb = 0, mine = 0;
-    for (int s = lane; s < a.B; s += 32) {
-        const int pages = q4_pages(a, s), c = pages > 0 ? pages + kQ4Switch : 0;
-        PC += c;
-        cb += s < b ? c : 0;
-        mine += s == b ? pages : 0;
+    if (!a.table) {
+#pragma unroll 1
+        for (int base = 0; base < a.B; base += 32 * kQ4Scan)
+#pragma unroll
+            for (int i = 0; i < kQ4Scan; ++i) {
+                if (base + 32 * i >= a.B) break;
+                const int s = base + 32 * i + lane;
+                const int pages = s < a.B ? q4_pages(a, s, a.seqused_k[s]) : 0, c = pages > 0 ? pages + kQ4Switch : 0;
+                PC += c;
+                cb += s < b ? c : 0;
+                mine += s == b ? pages : 0;
+            }
+        PC = __reduce_add_sync(0xffffffffu, PC);
+        cb = __reduce_add_sync(0xffffffffu, cb);
+        mine = __reduce_add_sync(0xffffffffu, mine);
     }
-    PC = __reduce_add_sync(0xffffffffu, PC);
-    cb = __reduce_add_sync(0xffffffffu, cb);
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    const int share = q4_share(PC, a);
-    const int c0 = (hb * PC + cb + kQ4Switch) / share;            // the CTAs of its first and last page
-    const int ns = live && mine > 0 ? (hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1 : 0;
-    const long long first = (((long long)c0 + hb * a.B + b) * a.HB + h) * a.rows + row;
+    int ns = 0;
+    long long first = 0;
+    auto slots = [&]() {
+        const int share = q4_share(PC, a);
+        const int c0 = (hb * PC + cb + kQ4Switch) / share;        // the CTAs of its first and last page
+        ns = live && mine > 0 ? (hb * PC + cb + kQ4Switch + mine - 1) / share - c0 + 1 : 0;
+        first = (((long long)c0 + hb * a.B + b) * a.HB + h) * a.rows + row;
+    };
+    if (!a.table) slots();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (a.table) {
+        const int2 x = a.table[b];
+        mine = x.x;
+        cb = x.y;
+        PC = a.table[a.B].y;
+        slots();
+    }
     const long long step = (long long)a.HB * a.rows * a.wpr;      // rows between this warp's partials
     float M = -INFINITY, sum = 0.0f, acc[V];
     bool nan = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int s0 = sub; s0 < ns; s0 += N * a.wpr) {
         const long long at = first + (long long)s0 * a.HB * a.rows;
         float x[N], y[N][V];

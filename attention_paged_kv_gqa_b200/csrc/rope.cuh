@@ -47,30 +47,29 @@ struct RopeAngles {
 // The eight pairs 8 u .. 8 u + 7 of token t.
 __device__ __forceinline__ RopeAngles rope_angles(const RopeTable& r, long long t, long long total, int u, int seq_pos) {
     const int half = r.rot / 2;
-    // the token's position on every axis, and the axes of the eight pairs
-    int p[kRopeMaxAxes];
+    // the token's position on every axis, and the axes of the eight pairs (all loads first)
+    int p[kRopeMaxAxes], ax[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int a = 0; a < kRopeMaxAxes; ++a) p[a] = a < r.axes ? r.positions ? __ldg(r.positions + a * total + t) : seq_pos : 0;
+    if (r.pair_axis) {
+        const int4 a0 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u));
+        const int4 a1 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u + 4));
+        ax[0] = a0.x, ax[1] = a0.y, ax[2] = a0.z, ax[3] = a0.w, ax[4] = a1.x, ax[5] = a1.y, ax[6] = a1.z, ax[7] = a1.w;
+    }
 #pragma unroll
     for (int a = 0; a < kRopeMaxAxes; ++a)
         if (p[a] < 0 || p[a] >= r.max_pos) {
             record_data_error(kErrRopePosition);       // reported, the nearest row used
             p[a] = min(max(p[a], 0), r.max_pos - 1);
         }
-    int ax[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     bool one = true;
-    if (r.pair_axis) {
-        const int4 a0 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u));
-        const int4 a1 = __ldg(reinterpret_cast<const int4*>(r.pair_axis + 8 * u + 4));
-        ax[0] = a0.x, ax[1] = a0.y, ax[2] = a0.z, ax[3] = a0.w, ax[4] = a1.x, ax[5] = a1.y, ax[6] = a1.z, ax[7] = a1.w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (ax[i] < 0 || ax[i] >= r.axes) {
-                record_data_error(kErrRopeAxis);
-                ax[i] = 0;
-            }
-            one = one && ax[i] == ax[0];
+    for (int i = 0; i < 8; ++i) {
+        if (ax[i] < 0 || ax[i] >= r.axes) {
+            record_data_error(kErrRopeAxis);
+            ax[i] = 0;
         }
+        one = one && ax[i] == ax[0];
     }
     auto place = [&](int a) { return a == 0 ? p[0] : a == 1 ? p[1] : a == 2 ? p[2] : p[3]; };
     RopeAngles g;

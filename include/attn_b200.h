@@ -572,9 +572,9 @@ attn_status_t attn_decode_paged_q4(
  * max_seqlen_q) and the newest of its seqused_k[b] cached tokens; mask NONE or
  * CAUSAL, window_left and softcap as there; lse [Hq, total_q] fp32 or NULL.
  *   total_k      at least the sum of seqused_k: rows of the workspace (if it is less,
- *                code 531 is reported and the last tokens are left out).
+ *                code 531 is reported, and the last tokens may be left out).
  *   workspace    >= attn_fwd_q4_workspace_size(...) bytes, 16-byte aligned; as above.
- * Up to 64 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
+ * Up to 128 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
  * pages as they are; more, to bf16 rows that the call reads back first.
  */
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int num_heads_q, int num_heads_kv,
