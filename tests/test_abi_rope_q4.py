@@ -130,8 +130,8 @@ def test_workspace_sizes(L):
     assert L.attn_decode_q4_workspace_size(2, 130, 2, 128) == 0
     small, large = (L.attn_decode_q4_workspace_size(b, 32, 8, 128) for b in (1, 64))
     assert 0 < small < large
-    # past 64 query rows per KV head the packed bf16 rows of K and V
-    assert L.attn_fwd_q4_workspace_size(2, 17, 8, 2, 128, 100000) >= 2 * 100000 * 2 * 128 * 2
+    # past 128 query rows per KV head the packed bf16 rows of K and V
+    assert L.attn_fwd_q4_workspace_size(2, 33, 8, 2, 128, 100000) >= 2 * 100000 * 2 * 128 * 2
     assert L.attn_fwd_q4_workspace_size(2, 16, 8, 2, 128, 100000) < 2 * 100000 * 2 * 128 * 2
     assert L.attn_fwd_q4_workspace_size(2, -1, 8, 2, 128, 1000) == 0
 

@@ -9,7 +9,7 @@ their tolerances:
        (2^-18 of the same)
   LSE  the fp32 sum of D products of magnitude |q| 15 step (truncating adds,
        2^-22 each at most of the running sum) plus 2^-18
-The packed path past 64 query rows rounds its probabilities to bf16 (the library's
+The packed path past 128 query rows rounds its probabilities to bf16 (the library's
 tensor-core forward): 2e-2 and 1e-3, its tolerances elsewhere.
 """
 import math
@@ -473,7 +473,7 @@ def run_fwd(lens, qs, Hq, Hkv, D, group, causal=True, window=-1, softcap=0.0, se
     s = 1 / math.sqrt(D)
     o_ref, lse_ref = reference(q, cache, bt, lens, cu_q, s, causal, window, softcap)
     tol_o, tol_lse = tolerances(q, cache, s)
-    if max(qs) * (Hq // Hkv) > 64:
+    if max(qs) * (Hq // Hkv) > 128:
         tol_o, tol_lse = TOL_O_PACKED, TOL_LSE_PACKED
     check(o, lse, o_ref, lse_ref, tol_o, tol_lse)
 
@@ -495,6 +495,32 @@ def test_fwd_window_softcap(qs, window, softcap):
 def test_fwd_more_queries_than_keys(qs):
     run_fwd([2, 0], qs, 4, 1, 64, 64, seed=30)
     run_fwd([2, 0], qs, 4, 1, 64, 64, seed=31, causal=False)
+
+
+@pytest.mark.parametrize("Hq,Hkv,qs", [(8, 2, [17, 32, 0, 1, 25]), (8, 8, [128, 9, 100, 0, 65]), (12, 3, [3, 24, 31, 2, 8]),
+                                       (8, 1, [16, 2, 1, 9, 12]), (14, 2, [18, 5, 9, 1, 16]), (5, 5, [9, 16, 17, 33, 0])])
+@pytest.mark.parametrize("D,group,causal", [(64, 64, True), (128, 32, True), (128, 128, False)])
+def test_fwd_row_tiles(Hq, Hkv, qs, D, group, causal):
+    # up to 128 query rows per KV head, in tiles that a sequence fills, half fills or leaves empty
+    run_fwd([37, 500, 20, 0, 163], qs, Hq, Hkv, D, group, causal=causal, seed=Hq)
+
+
+@pytest.mark.parametrize("B", [127, 128, 129, 300])
+def test_fwd_many_short_sequences(B):
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 70, (B,), generator=g).tolist()
+    qs = torch.randint(0, 4, (B,), generator=g).tolist()
+    run_fwd(lens, qs, 8, 2, 64, 32, seed=B)
+
+
+def test_fwd_total_k_past_the_page_stream():
+    lens = [100, 34]
+    bt, pool = table_for(lens)
+    cache = dev(*R.fill((pool, 2, 16, 32), 32, 33))
+    q = randn((80, 4, 64), 34).to(DEV)
+    A.attn_fwd_varlen_paged_q4(q, *cache, block_table=bt.to(DEV), cu_seqlens_q=i32([0, 10, 80]).to(DEV), max_seqlen_q=70,
+                               seqused_k=i32(lens).to(DEV), total_k=120, mask=A.MASK_CAUSAL)
+    assert A.attn_device_error() == 531
 
 
 def test_fwd_total_k():
