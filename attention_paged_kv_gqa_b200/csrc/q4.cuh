@@ -107,6 +107,13 @@ __device__ __forceinline__ float q4_zero(uint32_t meta) { return __uint_as_float
 // smallest and largest are found across its group / 8 lanes, a K word is one
 // lane's eight codes, and the V pieces are regrouped among the four lanes that
 // hold the dims 32 u .. 32 u + 31.
+// Bound by HBM and, close behind, by the issue of instructions (55 % of the slots,
+// the logic pipe 47 %): 16955 tokens of 32 + 8 + 8 heads of 128, 70 to 74 us, of
+// which the bytes take 57.  It was 106: the division by the step became a product
+// with its approximate reciprocal whose ties are made exact (see q4_nearest), the
+// minimum and the negated maximum of a group travel in one register, and codes
+// are put together by fused multiply-adds.  Four passes' loads in flight (two:
+// 4 us more); 64 or 256 threads a block: 12 and 18 us more.
 template <int D, int GS>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_q4_kernel(const RopeAppendArgs a) {
     constexpr int U = D / 16, HP = 32 / U;        // q: units, heads at once
@@ -300,7 +307,10 @@ __device__ __forceinline__ uint32_t q4_steps(uint32_t m2) { return m2 & 0xfff0ff
 __device__ __forceinline__ uint32_t q4_zeros(uint32_t m2) { return (m2 & 0x000f000fu) | 0x43004300u; }
 
 // The rows of packed K and V from 4-bit pages: a warp takes the K and V tile of
-// one page and head.  The values are bf16 numbers, so nothing is lost.
+// one page and head.  The values are bf16 numbers, so nothing is lost.  HBM bound
+// by what it writes (4 bytes for each byte read): 59000 tokens of 8 heads of 128,
+// 65 us, 4.6 TB/s; the arithmetic is two packed bf16 operations for two values.  A
+// warp looks its next page up while it unpacks this one.
 template <int D, int GS>
 __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
     constexpr int W = D / 32, G = D / GS;
@@ -439,16 +449,19 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 }
 
 // ---------------------------------------------------------------- attention
-// A few query rows per sequence (tokens x query heads of a KV head, in RT tiles of
-// eight) over 4-bit pages: the page stream of decode.cuh with another consumer.
+// A few query rows per sequence (tokens x query heads of a KV head) over 4-bit pages: the
+// page stream of decode.cuh with another consumer.
 //
-// The pages of the batch, for one block of HB KV heads after another, are cut
-// into one contiguous equal share per CTA.  A page's HB tiles of K, V and their
-// metas are four contiguous runs, fetched by four bulk copies into a ring of
-// stages.  Of the SUB warps of a KV head and row tile each takes every SUB-th page and
-// keeps an online softmax of its own; where a sequence or the share ends they are joined
-// through shared memory, and the partial (O normalised, LSE) goes to slot
-// CTA + sequence for the combine kernel.
+// Split.  The pages of the batch, for one block of HB KV heads after another, are cut into
+// one contiguous share of equal cost per CTA, a change of sequence counted as kQ4Switch
+// pages.  A page's HB tiles of K, V and their metas are four contiguous runs, which three
+// producer warps fetch by bulk copies into a ring of stages; a fourth prepares the queries
+// of the share's next sequence.  The query rows are in RT tiles of 8 NT, and of the SUB warps
+// of a KV head and tile each takes every SUB-th page, two at a time (with NT = 2 one, whose
+// two tiles' chains run side by side), and keeps an online softmax of its own.  Where a
+// sequence or the share ends they are joined through shared memory, in a fixed order, and
+// the partial (O normalised, LSE) goes to slot CTA + sequence for the combine kernel, which
+// follows as a programmatic dependent.  No atomics: the result does not depend on timing.
 //
 // Score: s = step (q . c - zero sum q), c the codes: the code, shifted to the
 // low or second nibble of a 16-bit half, IS the f16 number c 2^-24 or c 2^-20
@@ -456,13 +469,29 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // shift.  q is exact in f16 after a power of two per row, divided by 16 for the
 // dims that meet second nibbles.  The output: O = sum_j w_j c_j - sum_j w_j zero_j
 // with w_j = p_j step_j, again on the codes as they are; w is rounded to f16
-// (11 bits) after a power of two that keeps the largest step in range.  Groups
-// smaller than the head repeat the two sums per group.
+// (what the MMA takes: at most 2^-11 of each weight, an eighth of the rounding of
+// the bf16 output) after a power of two that keeps the largest step in
+// range; everything else is held in fp32.  Groups smaller than the head repeat the
+// two sums per group.
 // The first sum is far larger than the difference where p is spread over many
 // keys, and the tensor cores truncate when they add; every 16 pages the second
-// sum is therefore taken out of the accumulators, which stay near their final size.
-// The running maximum moves only when a score exceeds it by 2^8, which a page
-// shows by one vote.
+// sum is therefore taken out of the accumulators, which stay near their final size
+// (every 4 or every 64 pages take the same time).  The running maximum moves only
+// when a score exceeds it by 2^8, which a page shows by one vote (48.6 us on the
+// first case below if it moves with every larger score, against 47).
+//
+// Bound.  Bytes would take 20 us for 32 sequences of 4100 keys (32 + 8 heads of 128, groups
+// of 128) and 35 us for 3 of 65000 (64 + 8, groups of 32); the calls take 43 to 46 and 70 to
+// 73.  About 14 us are fixed: 4 to 5 until the first page is there (launch, lengths, table,
+// page), 1.5 to 2 for the join, 4 to 6 for the combine kernel.  A page of four heads then
+// costs 0.27 us of a CTA's time, where its bytes take 0.20: taking the codes apart keeps the
+// logic pipe at 51 and 61 % of its rate over the whole call, and the chain from score to
+// weight does not leave it busy throughout.  The tensor pipe is at 20 %, DRAM at half.  A
+// change of sequence costs 3 to 4 us (kQ4Switch: with 0, 6 and 20 in place of 13 the first
+// case took 51, 49 and 47 us against 47, 600 sequences of 100 keys 149, 123 and 113 against 114).
+// Tried and slower: MMAs on e4m3 codes (the warp form is emulated: 1.6 times), shifts on the
+// multiplier, the next pages' scores ahead of this pair's softmax (with twelve warps 49 us
+// against 45).
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
 constexpr int kQ4Recentre = 16;          // pages
 constexpr int kQ4Producers = 4;          // warps that fetch K, V, their metas, the queries
@@ -1254,8 +1283,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
     }
 }
 
-// Joins the partials: a.wpr warps per output row.  The partials of sequence b and
-// head block hb sit in slots c + hb B + b for the CTAs c whose shares covered it.
+// Joins the partials: a.wpr warps per output row (one for each eight partials, whose loads
+// are in flight together): bound by its launch and two round trips, 4 to 6 us.  The partials
+// of sequence b and head block hb sit in slots c + hb B + b for the CTAs c whose shares
+// covered it.
 template <int D>
 __global__ void __launch_bounds__(256) q4_combine_kernel(const Q4AttnArgs a) {
     constexpr int V = D / 32;            // columns of a lane
