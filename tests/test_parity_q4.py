@@ -452,7 +452,7 @@ def test_calls_on_a_given_stream():
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 64)])
 @pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 2), (12, 12), (32, 8)])
 def test_decode_many_short_sequences(D, group, Hq, Hkv):
-    """Shares that hold many sequences, some without keys: partials per warp, and their joins."""
+    """Shares that hold many sequences, some without keys, and their joins."""
     g = torch.Generator().manual_seed(Hq)
     lens = [int(n) for n in torch.randint(0, 60, (170,), generator=g)]
     lens[5:9] = [0, 0, 0, 1]
