@@ -2,6 +2,8 @@
 // appends and the 4-bit cache (included by attn_api.cu, whose helpers it uses).
 #pragma once
 
+#include <climits>
+
 #include "q4.cuh"
 
 namespace {
@@ -171,12 +173,13 @@ attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, s
 
 template <int D, int GS>
 attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
-    // A page and head per warp at a time; every block builds the tables, so no more blocks than
-    // two to an SM, which write neighbouring rows closer in time than more do (8 sequences of
-    // 16000 tokens: 132 us, at four to an SM 150, with a block for every eight pages and heads
-    // 131; 512 of 100: 69.6, 69.3 and 94; below 30000 tokens all alike).
-    const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv;
-    const int grid = (int)std::max<long long>(1, std::min<long long>((items + 7) / 8, (long long)sms * 2));
+    // A page and head per warp.  Every block builds the tables: that is cheap for up to 16
+    // sequences, and a block then takes eight (8 sequences of 16000 tokens 111 us, with two
+    // lasting blocks to an SM 127; 16 of 3688: 55.5 and 60.5; 16 of 300: 11.3 and 12.3).  For
+    // more sequences two lasting blocks to an SM (32 of 500: 18.4 us, in eights 20.4; 512 of 100:
+    // 59 and 90; with three 61, with four 73).
+    const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv, blocks = (items + 7) / 8;
+    const int grid = (int)std::max<long long>(1, std::min<long long>(blocks, a.B <= 16 ? INT_MAX : (long long)sms * 2));
     q4_gather_kernel<D, GS><<<grid, 256, 2 * (a.B + 1) * sizeof(int), st>>>(a);
     return launch_status();
 }
