@@ -583,28 +583,30 @@ def _heads(t, shape, dev, where, name):
     return _pair(row, head)
 
 
-def _call(fn, dev, stream, *args):
-    """fn(*args, stream) with dev current (stream None: its current stream)."""
+def _call(fn, dev, *args):
+    """fn(*args, the current stream of dev) with dev current."""
     i = dev.index
-    if stream is not None:
-        raw = stream.cuda_stream
-    elif _raw_stream is not None:
-        raw = _raw_stream(i)
-    else:
-        raw = torch.cuda.current_stream(dev).cuda_stream
+    raw = _raw_stream(i) if _raw_stream is not None else torch.cuda.current_stream(dev).cuda_stream
     if _current_device() != i:
         with torch.cuda.device(dev):
             return fn(*args, raw)
     return fn(*args, raw)
 
 
-def _kept(stream, *tensors):
-    """Memory taken here for a call on another stream than torch's current one is not handed out
-    again before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
+def _on(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` current.  What it allocates is that stream's memory (another
+    stream's may still be in use there), and is not handed out again before the stream that was
+    current is done with it."""
+    dev = next((a.device for a in args if isinstance(a, torch.Tensor)), stream.device)
+    _need(stream.device == dev, call.__name__, "the stream is of %s, the tensors are on %s" % (stream.device, dev))
+    here = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    if here != stream:
+        for t in out:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(here)
+    return out
 
 
 def _at(t):
@@ -644,6 +646,9 @@ def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=Fals
     pairs columns (2 i, 2 i + 1) in place of (i, i + rot_dim / 2).  inverse turns the other
     way: the gradient of the forward rotation.  out_q / out_k may be q / k themselves.
     """
+    if stream is not None:
+        return _on(stream, attn_rope, q, k, cos_sin=cos_sin, positions=positions, pair_axis=pair_axis,
+                   interleaved=interleaved, inverse=inverse, out_q=out_q, out_k=out_k)
     where = "attn_rope"
     (total, Hq, D), dev = _cuda(q, where, "q")
     sq = _heads(q, (total, Hq, D), dev, where, "q")
@@ -664,10 +669,9 @@ def attn_rope(q, k=None, *, cos_sin, positions, pair_axis=None, interleaved=Fals
         _need(out_k is None, where, "out_k without k")
     if total == 0:
         return out_q, out_k
-    st = _call(lib().attn_rope, dev, stream, q.data_ptr(), out_q.data_ptr(), _at(k), _at(out_k), sq, so, sk, sko, total,
+    st = _call(lib().attn_rope, dev, q.data_ptr(), out_q.data_ptr(), _at(k), _at(out_k), sq, so, sk, sko, total,
                Hq, Hkv, D, *rope, 1 if interleaved else 0, 1 if inverse else 0)
     _check(st, where)
-    _kept(stream, out_q, out_k)
     return out_q, out_k
 
 
@@ -701,13 +705,6 @@ def _append_args(q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, sequse
     return dev, total, Hq, Hkv, D, B, mbps, sq, sk, sv, out_q, seqused_k_out
 
 
-def _same_lengths(seqused_k, used, dev, stream):
-    """The lengths after an append of nothing (an empty tensor has no address to pass)."""
-    with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else stream):
-        used.copy_(seqused_k)
-    return used
-
-
 def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, seqused_k, *, cos_sin=None,
                               positions=None, pair_axis=None, interleaved=False, cu_seqlens_new=None,
                               descale_q=None, descale_k=None, descale_v=None, out_q=None,
@@ -717,6 +714,11 @@ def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, se
 
     q may be None (q_out is then None).  positions None: each token's position in the cache.
     """
+    if stream is not None:
+        return _on(stream, attn_kv_append_rope_paged, q, k_new, v_new, k_cache, v_cache, block_table, seqused_k,
+                   cos_sin=cos_sin, positions=positions, pair_axis=pair_axis, interleaved=interleaved,
+                   cu_seqlens_new=cu_seqlens_new, descale_q=descale_q, descale_k=descale_k,
+                   descale_v=descale_v, out_q=out_q, seqused_k_out=seqused_k_out)
     where = "attn_kv_append_rope_paged"
     n, bs, _, _ = _dims(k_cache, 4, where, "k_cache")
     fp8 = k_cache.dtype is torch.float8_e4m3fn
@@ -736,13 +738,12 @@ def attn_kv_append_rope_paged(q, k_new, v_new, k_cache, v_cache, block_table, se
         descale_q = descale_k = descale_v = None
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
     if total == 0:
-        return out_q, _same_lengths(seqused_k, used, dev, stream)
-    st = _call(lib().attn_kv_append_rope_paged, dev, stream, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
+        return out_q, used.copy_(seqused_k)      # (an empty tensor has no address to pass)
+    st = _call(lib().attn_kv_append_rope_paged, dev, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
                sv, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), mbps, n, bs, _at(cu_seqlens_new),
                seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, *rope, 1 if interleaved else 0,
                FP8_E4M3 if fp8 else BF16, _at(descale_q), _at(descale_k), _at(descale_v))
     _check(st, where)
-    _kept(stream, out_q, used)
     return out_q, used
 
 
@@ -770,6 +771,10 @@ def attn_kv_append_paged_q4(q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, b
     [num_blocks, Hkv, 16, D / group_size], group_size 32, 64 or 128 (the format is described
     in the header).
     """
+    if stream is not None:
+        return _on(stream, attn_kv_append_paged_q4, q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, block_table,
+                   seqused_k, cos_sin=cos_sin, positions=positions, pair_axis=pair_axis, interleaved=interleaved,
+                   cu_seqlens_new=cu_seqlens_new, out_q=out_q, seqused_k_out=seqused_k_out)
     where = "attn_kv_append_paged_q4"
     dev, total, Hq, Hkv, D, B, mbps, sq, sk, sv, out_q, used = _append_args(
         q, k_new, v_new, block_table, seqused_k, cu_seqlens_new, seqused_k_out, out_q, _BF16, where)
@@ -778,13 +783,12 @@ def attn_kv_append_paged_q4(q, k_new, v_new, k_cache, v_cache, k_meta, v_meta, b
         _need(False, where, "k_new and the cache have different heads")
     rope = _rope_args(cos_sin, positions, pair_axis, total, dev, where, True)
     if total == 0:
-        return out_q, _same_lengths(seqused_k, used, dev, stream)
-    st = _call(lib().attn_kv_append_paged_q4, dev, stream, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
+        return out_q, used.copy_(seqused_k)      # (an empty tensor has no address to pass)
+    st = _call(lib().attn_kv_append_paged_q4, dev, _at(q), _at(out_q), k_new.data_ptr(), v_new.data_ptr(), sq, sk,
                sv, k_cache.data_ptr(), v_cache.data_ptr(), k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(),
                mbps, n, bs, _at(cu_seqlens_new), seqused_k.data_ptr(), used.data_ptr(), B, total, Hq, Hkv, D, gs, *rope,
                1 if interleaved else 0)
     _check(st, where)
-    _kept(stream, out_q, used)
     return out_q, used
 
 
@@ -794,6 +798,9 @@ def attn_kv_gather_paged_q4(k_cache, v_cache, k_meta, v_meta, block_table, cu_se
 
     Sequence b's tokens starts[b] .. (None: 0 ..) go to rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1.
     """
+    if stream is not None:
+        return _on(stream, attn_kv_gather_paged_q4, k_cache, v_cache, k_meta, v_meta, block_table, cu_seqlens, total,
+                   starts=starts, out_k=out_k, out_v=out_v)
     where = "attn_kv_gather_paged_q4"
     B = _dims(cu_seqlens, 1, where, "cu_seqlens")[0] - 1
     _need(B >= 0 and cu_seqlens.is_cuda, where, "cu_seqlens must be a CUDA tensor of B + 1 entries")
@@ -816,11 +823,10 @@ def attn_kv_gather_paged_q4(k_cache, v_cache, k_meta, v_meta, block_table, cu_se
         _tensor(out_v, _BF16, shape, dev, where, "out_v")
     if total == 0:
         return out_k, out_v
-    st = _call(lib().attn_kv_gather_paged_q4, dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), k_meta.data_ptr(),
+    st = _call(lib().attn_kv_gather_paged_q4, dev, k_cache.data_ptr(), v_cache.data_ptr(), k_meta.data_ptr(),
                v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, cu_seqlens.data_ptr(), _at(starts), B, total, Hkv,
                D, gs, out_k.data_ptr(), out_v.data_ptr())
     _check(st, where)
-    _kept(stream, out_k, out_v)
     return out_k, out_v
 
 
@@ -856,6 +862,10 @@ def attn_decode_paged_q4(q, k_cache, v_cache, k_meta, v_meta, block_table, sequs
                          window_left=-1, softcap=0.0, out=None, lse=None, workspace=None,
                          return_lse=True, stream=None):
     """attn_decode_paged over a 4-bit cache: q [B, Hq, D] bf16 -> (o [B, Hq, D] bf16, lse [B, Hq] fp32)."""
+    if stream is not None:
+        return _on(stream, attn_decode_paged_q4, q, k_cache, v_cache, k_meta, v_meta, block_table, seqused_k,
+                   scale=scale, window_left=window_left, softcap=softcap, out=out, lse=lse,
+                   workspace=workspace, return_lse=return_lse)
     where = "attn_decode_paged_q4"
     (B, Hq, D), dev = _cuda(q, where, "q")
     n, bs, Hkv, Dc, gs = _q4_cache(k_cache, v_cache, k_meta, v_meta, dev, where)
@@ -869,12 +879,11 @@ def attn_decode_paged_q4(q, k_cache, v_cache, k_meta, v_meta, block_table, sequs
         return out, lse
     L = lib()
     workspace = _space(workspace, L.attn_decode_q4_workspace_size(B, Hq, Hkv, D), q, dev, where)
-    st = _call(L.attn_decode_paged_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    st = _call(L.attn_decode_paged_q4, dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, seqused_k.data_ptr(), B, Hq, Hkv,
                D, gs, _scale(scale), int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(),
                workspace.numel())
     _check(st, where)
-    _kept(stream, out, lse, workspace)
     return out, lse
 
 
@@ -886,6 +895,11 @@ def attn_fwd_varlen_paged_q4(q, k_cache, v_cache, k_meta, v_meta, *, block_table
 
     total_k: at least the sum of seqused_k (rows of the workspace); mask NONE or CAUSAL.
     """
+    if stream is not None:
+        return _on(stream, attn_fwd_varlen_paged_q4, q, k_cache, v_cache, k_meta, v_meta,
+                   block_table=block_table, cu_seqlens_q=cu_seqlens_q, max_seqlen_q=max_seqlen_q,
+                   seqused_k=seqused_k, total_k=total_k, mask=mask, scale=scale, window_left=window_left,
+                   softcap=softcap, out=out, lse=lse, workspace=workspace, return_lse=return_lse)
     where = "attn_fwd_varlen_paged_q4"
     (total_q, Hq, D), dev = _cuda(q, where, "q")
     B = _dims(seqused_k, 1, where, "seqused_k")[0]
@@ -901,10 +915,9 @@ def attn_fwd_varlen_paged_q4(q, k_cache, v_cache, k_meta, v_meta, *, block_table
         return out, lse
     L, most, total_k = lib(), int(max_seqlen_q), int(total_k)
     workspace = _space(workspace, L.attn_fwd_q4_workspace_size(B, most, Hq, Hkv, D, total_k), q, dev, where)
-    st = _call(L.attn_fwd_varlen_paged_q4, dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    st = _call(L.attn_fwd_varlen_paged_q4, dev, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                k_meta.data_ptr(), v_meta.data_ptr(), block_table.data_ptr(), mbps, n, bs, cu_seqlens_q.data_ptr(),
                seqused_k.data_ptr(), B, total_q, total_k, most, Hq, Hkv, D, gs, _scale(scale), int(mask),
                int(window_left), float(softcap), out.data_ptr(), _at(lse), workspace.data_ptr(), workspace.numel())
     _check(st, where)
-    _kept(stream, out, lse, workspace)
     return out, lse

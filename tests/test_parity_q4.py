@@ -449,6 +449,33 @@ def test_calls_on_a_given_stream():
     assert float((outs[-1][1] - want[1].t()).abs().max()) <= TOL_LSE_PACKED
 
 
+def test_a_given_stream_takes_memory_of_its_own():
+    """What the current stream may still read is not handed to a call on another stream."""
+    lens = [64, 64]
+    bt, pool = table_for(lens, seed=79)
+    cache = dev(*R.fill((pool, 2, 16, 64), 64, 80))
+    q, dbt, dl = randn((2, 8, 128), 81).to(DEV), bt.to(DEV), i32(lens).to(DEV)
+    cu, cs = i32([0, 64, 128]).to(DEV), R.table(64, 128).to(DEV)
+    pos, s = i32([3, 5]).to(DEV), torch.cuda.Stream()
+    kv = randn((2, 2, 128), 82).to(DEV)
+    calls = [lambda: A.attn_decode_paged_q4(q, *cache, dbt, dl, stream=s),
+             lambda: A.attn_fwd_varlen_paged_q4(q, *cache, block_table=dbt, cu_seqlens_q=i32([0, 1, 2]).to(DEV),
+                                                max_seqlen_q=1, seqused_k=dl, total_k=128, mask=1, stream=s),
+             lambda: A.attn_rope(q, kv, cos_sin=cs, positions=pos, stream=s),
+             lambda: A.attn_kv_append_paged_q4(q, kv, kv, *cache, dbt, dl - 1, cos_sin=cs, stream=s),
+             lambda: A.attn_kv_gather_paged_q4(*cache, dbt, cu, 128, stream=s)]
+    for call in calls:
+        torch.cuda.synchronize()
+        shapes = [(t.shape, t.dtype) for t in call()]
+        torch.cuda.synchronize()
+        olds = [torch.zeros(shape, dtype=dtype, device=DEV) for shape, dtype in shapes]
+        places = {t.data_ptr() for t in olds}
+        del olds
+        assert not places & {t.data_ptr() for t in call()}
+    torch.cuda.synchronize()
+    assert A.attn_device_error() == 0
+
+
 @pytest.mark.parametrize("D,group", [(64, 32), (128, 64)])
 @pytest.mark.parametrize("Hq,Hkv", [(2, 1), (8, 2), (12, 12), (32, 8)])
 def test_decode_many_short_sequences(D, group, Hq, Hkv):
