@@ -486,6 +486,14 @@ def test_decode_many_short_sequences(D, group, Hq, Hkv):
     run_decode(lens, Hq, Hkv, D, group, seed=80 + Hq)
 
 
+def test_decode_largest_batch():
+    g = torch.Generator().manual_seed(3)
+    lens = [int(n) for n in torch.randint(0, 40, (4096,), generator=g)]
+    run_decode(lens, 4, 2, 64, 64, seed=91)
+    with pytest.raises(A.AttnError):
+        run_decode([1] * 4097, 4, 2, 64, 64, seed=92)
+
+
 # ---------------------------------------------------------------- several queries
 def run_fwd(lens, qs, Hq, Hkv, D, group, causal=True, window=-1, softcap=0.0, seed=0, total_k=None):
     bt, pool = table_for(lens, seed=seed)
