@@ -548,6 +548,37 @@ def test_fwd_many_short_sequences(B):
     run_fwd(lens, qs, 8, 2, 64, 32, seed=B)
 
 
+@pytest.mark.parametrize("qs", [[3, 3, 2], [40, 50, 33]])
+def test_fwd_ignores_its_neighbours_and_the_workspace(qs):
+    """NaN and infinite values of one sequence, and a workspace full of NaN, reach no other sequence."""
+    Hq, Hkv, D, group, lens = 8, 2, 128, 64, [70, 37, 0]
+    bt, pool = table_for(lens, seed=60)
+    cache = R.fill((pool, Hkv, 16, D // 2), group, 61)
+    for meta in cache[2:]:                            # all of sequence 1 stands for NaN
+        for page in bt[1, :3].tolist():
+            meta[page] = 0x7fc0
+    q = randn((sum(qs), Hq, D), 62)
+    cu = np.concatenate([[0], np.cumsum(qs)])
+    need = A.attn_fwd_q4_workspace_size(3, max(qs), Hq, Hkv, D, 500)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    o, lse = A.attn_fwd_varlen_paged_q4(q.to(DEV), *dev(*cache), block_table=bt.to(DEV), cu_seqlens_q=i32(cu).to(DEV),
+                                        max_seqlen_q=max(qs), seqused_k=i32(lens).to(DEV), total_k=500, mask=1, workspace=ws)
+    assert A.attn_device_error() == 0
+    first = R.fill((pool, Hkv, 16, D // 2), group, 61)
+    o_ref, lse_ref = reference(q[:qs[0]], first, bt[:1], lens[:1], [0, qs[0]], D ** -0.5, True, -1, 0.0)
+    tol_o, tol_lse = tolerances(q, first, D ** -0.5)
+    if max(qs) * 4 > 128:
+        tol_o, tol_lse = TOL_O_PACKED, TOL_LSE_PACKED
+    check(o[:qs[0]], lse[:, :qs[0]], o_ref, lse_ref, tol_o, tol_lse)
+    assert o[cu[1]:cu[2]].isnan().any()
+    assert not o[cu[2]:].any() and bool((lse[:, cu[2]:] == -math.inf).all())
+
+
+def test_fwd_without_any_key_past_the_page_stream():
+    run_fwd([0, 0], [40, 50], 8, 2, 64, 32, seed=63)
+    run_fwd([2, 0, 1], [40, 50, 3], 8, 2, 128, 64, seed=64)
+
+
 def test_fwd_total_k_past_the_page_stream():
     lens = [100, 34]
     bt, pool = table_for(lens)
