@@ -1197,16 +1197,20 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                 over = over || mx[nt].x > thr[nt].x || mx[nt].y > thr[nt].y;
             }
             if (__any_sync(0xffffffffu, over)) {
-                top = __reduce_max_sync(0xffffffffu, top);
+                top = 0;
+#pragma unroll
+                for (int x = 0; x < NP; ++x)
+#pragma unroll
+                    for (int g = 0; g < G; ++g)
+                        top = max(top, max(vm0[x][g] < 0x7f80u ? vm0[x][g] : 0u, vm1[x][g] < 0x7f80u ? vm1[x][g] : 0u));
+                top = __reduce_max_sync(0xffffffffu, top);       // of the steps that are numbers
                 float resc = 1.0f;
                 if (top >= cap_meta) {
-                    // 2^ex <= step < 2^(ex + 1): beta puts it below 2^7 (a NaN needs none)
+                    // 2^ex <= step < 2^(ex + 1): beta puts it below 2^7
                     const int ex = (int)(top >> 7) - 127;
-                    if (ex < 128) {
-                        const float nb = __uint_as_float((uint32_t)(127 + 6 - ex) << 23);
-                        resc = nb / beta;
-                        beta = nb;
-                    }
+                    const float nb = __uint_as_float((uint32_t)(127 + 6 - ex) << 23);
+                    resc = nb / beta;
+                    beta = nb;
                     cap_meta = (uint32_t)(ex + 128) << 7;
                 }
 #pragma unroll

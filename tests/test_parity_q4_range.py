@@ -212,3 +212,21 @@ def test_strong_channel(device, n):
     one = randn((4000, 2, 128), 7)
     one[1234, 0, 5] *= 80
     run(randn((n, 8, 128), 8), randn((4000, 2, 128), 9), one, 128)
+
+
+# ---------------------------------------------------------------- NaN
+@gpu
+@pytest.mark.parametrize("n", [1, 2, 5])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 32), (128, 64)])
+@pytest.mark.parametrize("power", [-60, -20, 0, 8, 17, 60])
+@pytest.mark.parametrize("at", [0, 700])
+def test_nan_group_leaves_the_other_groups(device, n, D, group, power, at):
+    """One group of one key stands for NaN: its columns are NaN, the others what they were."""
+    L, Hkv = 900, 2
+    cache = cache_of(randn((L, Hkv, D), 10), (randn((L, Hkv, D), 11).float() * 2.0 ** power).to(torch.bfloat16), group)
+    cache[3][at // 16, 1, at % 16, 0] = 0x7FC0
+    q = randn((n, 8, D), 12)
+    o, lse = attend([q], [cache], [L], group)
+    want = Attention(q, cache, L, group)
+    assert torch.isnan(want.o[:, 4:, :group]).all() and int(torch.isnan(want.o).sum()) == n * 4 * group
+    want.check(o[0], lse[0])
