@@ -472,7 +472,8 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // shift.  q is exact in f16 after a power of two per row, divided by 16 for the
 // dims that meet second nibbles.  The output: O = sum_j w_j c_j - sum_j w_j zero_j
 // with w_j = p_j step_j, again on the codes as they are; w is rounded to f16 (what
-// the MMA takes) after a power of two that keeps the largest step in range;
+// the MMA takes) after a scale per row and group that follows the largest w, not the
+// largest step, which may belong to a key of no weight or to another group's columns;
 // everything else is held in fp32.  Both sums take the rounded w, so that its error,
 // at most 2^-11 of each weight, meets the value c - zero and not the code c: the
 // weights of keys of equal scores all err alike (with the sum of the zeros over the
@@ -497,7 +498,9 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // Tried and slower: MMAs on e4m3 codes (the warp form is emulated: 1.6 times), shifts on the
 // multiplier, the next pages' scores ahead of this pair's softmax (with twelve warps 49 us
 // against 45).
-constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum
+constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum, and w <= 2^8 of its own
+constexpr float kQ4Top = 7.0f;           // the largest w seen is 2^7 (one of 2^15 still fits)
+constexpr float kQ4Range = 111.0f;       // w's maximum is held at 2^-111 of p's or more: p scale <= 2^126
 constexpr int kQ4Recentre = 16;          // pages
 constexpr int kQ4Producers = 4;          // warps that fetch K, V, their metas, the queries
 constexpr int kQ4Scan = 4;               // sequences that a lane looks up at once
@@ -540,8 +543,8 @@ struct Q4Cfg {
     static constexpr int TILE = kPageRows * D / 2;              // bytes of a head's K or V tile
     static constexpr int META = kPageRows * (D / GS) * 2;       // bytes of its metas
     __host__ __device__ static constexpr int stage_bytes(int HB) { return 2 * HB * (TILE + META); }
-    // pairs that a lane exchanges: accumulators, maxima, sums, beta
-    static constexpr int PAIRS = D / 16 * 2 * NT + 2 * NT + 1;
+    // pairs that a lane exchanges: outputs, maxima, sums
+    static constexpr int PAIRS = D / 16 * 2 * NT + 2 * NT;
     // (U: heads x row tiles)
     __host__ __device__ static constexpr int merge_bytes(int U, int SUB) {
         return SUB > 1 ? U * ((SUB + 1) / 2) * 32 * PAIRS * 8 : 0;
@@ -550,9 +553,11 @@ struct Q4Cfg {
     static constexpr int QROWS = 1 + D / GS;
     static constexpr int FRAG = NT * (D / 32) * 512, ROWS = QROWS * 32 * NT;
     __host__ __device__ static constexpr int query_bytes(int U) { return U * (FRAG + ROWS); }
+    // a warp's scales: per row and group the limit of w, the factor of p and the maximum of w
+    static constexpr int SCALES = NT * (D / GS) * 8 * 3 * 4;
     __host__ __device__ static constexpr int table_bytes(int B) { return ((3 * B + 2) * 4 + 15) / 16 * 16; }
     __host__ __device__ static constexpr int smem_bytes(int HB, int U, int SUB, int B, int ns) {
-        return ns * stage_bytes(HB) + 2 * query_bytes(U) + merge_bytes(U, SUB) + table_bytes(B) + (2 * ns + 4) * 8;
+        return ns * stage_bytes(HB) + 2 * query_bytes(U) + merge_bytes(U, SUB) + U * SUB * SCALES + table_bytes(B) + (2 * ns + 4) * 8;
     }
 };
 
@@ -564,6 +569,9 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
         "l"(src), "r"(n), "r"(smem_u32(bar)), "l"(pol)
         : "memory");
 }
+
+// 1 / s of a sum of weights, or 0 without any; a NaN stays one.
+__device__ __forceinline__ float q4_over(float s) { return s > 0.0f ? 1.0f / s : s == s ? 0.0f : s; }
 
 // D += A B and D = A B (no accumulator to clear), not volatile: free to be scheduled.
 __device__ __forceinline__ void q4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -695,6 +703,8 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
     tail += 2 * QB;
     float* mrg = reinterpret_cast<float*>(tail);
     tail += C::merge_bytes(U, SUB);
+    float2* scales = reinterpret_cast<float2*>(tail);
+    tail += U * SUB * C::SCALES;
     int* prefix = reinterpret_cast<int*>(tail);      // [B + 1] pages before sequence b
     int* cost = prefix + (a.B + 1);                  // [B + 1] their cost
     int* lenv = cost + (a.B + 1);                    // [B]
@@ -905,9 +915,12 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
     float2 acc[MT][NT][2];               // sum w c: tile rows r8 in units of 2^-24, r8 + 8 of 2^-20
     float2 zac[NT][G];                   // sum w zero, this lane's keys
     float2 m[NT], l[NT];                 // minus the maximum (log2 units); sum, this lane's keys
-    float2 thr[NT];                      // the raw score that moves the maximum
-    float beta = 1.0f;                   // w = p step beta
-    uint32_t cap_meta = 0;               // metas below it have steps that beta keeps in range
+    // Per row and group, in shared memory: w_max, the largest log2 of p step seen (the maximum of
+    // the scores not taken off: acc stays in its units when m moves), and by it w = p beta step with
+    // beta = 2^(7 + max - w_max), and the limit of log2(p step) that moves it.
+    float2* const lim = scales + warp * (C::SCALES / 8) + t4;
+    float2* const beta = lim + NT * G * 4;
+    float2* const wmax = beta + NT * G * 4;
     int since = 0;
     auto reset = [&]() {
         const float2 zero2 = make_float2(0.0f, 0.0f);
@@ -918,13 +931,20 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt] = make_float2(-kQ4NoMax, -kQ4NoMax);
-            thr[nt] = make_float2(-INFINITY, -INFINITY);
             l[nt] = zero2;
 #pragma unroll
             for (int g = 0; g < G; ++g) zac[nt][g] = zero2;
         }
-        beta = 1.0f;
-        cap_meta = 16;                               // a step above zero
+        __syncwarp();
+        if (r8 == 0) {
+#pragma unroll
+            for (int i = 0; i < NT * G; ++i) {
+                lim[4 * i] = make_float2(INFINITY, INFINITY);        // (the first key moves m)
+                beta[4 * i] = make_float2(1.0f, 1.0f);
+                wmax[4 * i] = make_float2(kQ4NoMax, kQ4NoMax);
+            }
+        }
+        __syncwarp();
         since = 0;
     };
     auto over_rows = [&](float2 v) {                 // the sum over the lanes of a column
@@ -955,8 +975,23 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
     // the end of a sequence or of the share: join the SUB warps of the head, write the partial
     auto flush_partial = [&](int vb, int n) {
         recentre();
+        // this warp's output: acc, in units of w, over l
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) l[nt] = over_rows(l[nt]);
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] = over_rows(l[nt]);
+            const float2 inv = make_float2(q4_over(l[nt].x), q4_over(l[nt].y));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const float2 w = fadd2(wmax[4 * (nt * G + g)], m[nt]);
+                const float2 half = make_float2(ex2(0.5f * w.x), ex2(0.5f * w.y));     // (2^w may not be a float)
+                const float2 f = fmul2(inv, half);
+#pragma unroll
+                for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
+                    acc[c][nt][0] = fmul2(fmul2(fmul2(acc[c][nt][0], make_float2(131072.0f, 131072.0f)), f), half);  // 2^(24 - 7)
+                    acc[c][nt][1] = fmul2(fmul2(fmul2(acc[c][nt][1], make_float2(8192.0f, 8192.0f)), f), half);      // 2^(20 - 7)
+                }
+            }
+        }
         constexpr int FL = C::PAIRS;                 // pairs a lane exchanges
         const int slots = (SUB + 1) / 2;
         float2* mine = reinterpret_cast<float2*>(mrg) + unit * slots * 32 * FL;
@@ -977,14 +1012,10 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                     x[32 * (MT * NT + nt) * 2] = m[nt];
                     x[32 * ((MT * NT + nt) * 2 + 1)] = l[nt];
                 }
-                x[32 * (FL - 1)] = make_float2(beta, 0.0f);
             }
             asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
             if (sub < st && sub + st < SUB) {
                 const float2* x = mine + sub * 32 * FL + lane;
-                const float beta2 = x[32 * (FL - 1)].x, nb = fminf(beta, beta2);     // the larger steps' unit
-                const float r1 = nb / beta, r2 = nb / beta2;
-                beta = nb;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const float2 m2 = x[32 * (MT * NT + nt) * 2], l2 = x[32 * ((MT * NT + nt) * 2 + 1)];
@@ -992,9 +1023,12 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                     float2 f1 = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
                     float2 f2 = make_float2(ex2(mn.x - m2.x), ex2(mn.y - m2.y));
                     m[nt] = mn;
-                    l[nt] = ffma2(l[nt], f1, fmul2(l2, f2));
-                    f1 = fmul2(f1, make_float2(r1, r1));
-                    f2 = fmul2(f2, make_float2(r2, r2));
+                    f1 = fmul2(l[nt], f1);
+                    f2 = fmul2(l2, f2);
+                    l[nt] = fadd2(f1, f2);
+                    const float2 inv = make_float2(q4_over(l[nt].x), q4_over(l[nt].y));
+                    f1 = fmul2(f1, inv);
+                    f2 = fmul2(f2, inv);
 #pragma unroll
                     for (int c = 0; c < MT; ++c)
 #pragma unroll
@@ -1005,7 +1039,6 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
             asm volatile("bar.sync %0, %1;" ::"r"(1 + unit), "r"(32 * SUB) : "memory");
         }
         if (sub > 0) return;
-        const float back = 64.0f / beta;             // a power of two, within range for every step
         const long long base = (((long long)blockIdx.x + vb) * HB + h) * a.rows;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -1014,13 +1047,11 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                 const int row = row0 + nt * 8 + 2 * t4 + e;
                 if (row >= n * a.group) continue;
                 const float s = e ? l[nt].y : l[nt].x;
-                const float inv = s > 0.0f ? 1.0f / s : s == s ? 0.0f : s;    // a NaN stays one
-                const float lo = inv * 262144.0f, hi = inv * 16384.0f;        // 2^24 / 64, 2^20 / 64
                 float* rp = a.o_part + (base + row) * D;
 #pragma unroll
                 for (int c = 0; c < MT; ++c) {
-                    rp[16 * c + r8] = (e ? acc[c][nt][0].y : acc[c][nt][0].x) * lo * back;
-                    rp[16 * c + 8 + r8] = (e ? acc[c][nt][1].y : acc[c][nt][1].x) * hi * back;
+                    rp[16 * c + r8] = e ? acc[c][nt][0].y : acc[c][nt][0].x;
+                    rp[16 * c + 8 + r8] = e ? acc[c][nt][1].y : acc[c][nt][1].x;
                 }
                 if (r8 == 0)
                     a.lse_part[base + row] = s > 0.0f ? (log2f(s) - (e ? m[nt].y : m[nt].x)) * kLn2 : s == s ? -INFINITY : s;
@@ -1179,13 +1210,17 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                             }
                     }
             }
-            // does a score exceed its row's maximum by the slack, or a step the range?
-            uint32_t top = 0;
+            // Does a score exceed its row's maximum by the slack, or a weight its own?  (Of the weights a
+            // bound from above, the lane's largest score by its largest step, whose bits count 128 to the
+            // octave and stay at most 0.09 below its logarithm; a step of 0 counts as 2^-127, too little.)
+            bool over = false;
+            float top[G];
 #pragma unroll
-            for (int x = 0; x < NP; ++x)
-#pragma unroll
-                for (int g = 0; g < G; ++g) top = max(top, max(vm0[x][g], vm1[x][g]));
-            bool over = top >= cap_meta;
+            for (int g = 0; g < G; ++g) {
+                uint32_t most = max(vm0[0][g], vm1[0][g]);
+                if (NP > 1) most = max(most, max(vm0[NP - 1][g], vm1[NP - 1][g]));
+                top[g] = fmaf(__uint_as_float(most | 0x4b000000u), 0.0078125f, -65663.0f);
+            }
             float2 mx[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -1194,48 +1229,62 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                     mx[nt].x = fmax3(mx[nt].x, sc[NP - 1][nt][0].x, sc[NP - 1][nt][1].x);
                     mx[nt].y = fmax3(mx[nt].y, sc[NP - 1][nt][0].y, sc[NP - 1][nt][1].y);
                 }
-                over = over || mx[nt].x > thr[nt].x || mx[nt].y > thr[nt].y;
+                const float2 u = ffma2(mx[nt], kf[nt], m[nt]);
+                over = over || u.x > kQ4Slack || u.y > kQ4Slack;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const float2 w = fadd2(u, make_float2(top[g], top[g])), most = lim[4 * (nt * G + g)];
+                    over = over || w.x > most.x || w.y > most.y;
+                }
             }
             if (__any_sync(0xffffffffu, over)) {
-                top = 0;
-#pragma unroll
-                for (int x = 0; x < NP; ++x)
-#pragma unroll
-                    for (int g = 0; g < G; ++g)
-                        top = max(top, max(vm0[x][g] < 0x7f80u ? vm0[x][g] : 0u, vm1[x][g] < 0x7f80u ? vm1[x][g] : 0u));
-                top = __reduce_max_sync(0xffffffffu, top);       // of the steps that are numbers
-                float resc = 1.0f;
-                if (top >= cap_meta) {
-                    // 2^ex <= step < 2^(ex + 1): beta puts it below 2^7
-                    const int ex = (int)(top >> 7) - 127;
-                    const float nb = __uint_as_float((uint32_t)(127 + 6 - ex) << 23);
-                    resc = nb / beta;
-                    beta = nb;
-                    cap_meta = (uint32_t)(ex + 128) << 7;
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float2 y = mx[nt];
+                // (a NaN among the steps takes no part: it makes its weights and its group NaN)
+                auto largest = [&](float2 y) {       // over the keys of a column
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) {
                         y.x = fmaxf(y.x, __shfl_xor_sync(0xffffffffu, y.x, o));
                         y.y = fmaxf(y.y, __shfl_xor_sync(0xffffffffu, y.y, o));
                     }
+                    return y;
+                };
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 y = largest(mx[nt]);
                     const float2 mn = make_float2(fminf(m[nt].x, -y.x * kf[nt].x), fminf(m[nt].y, -y.y * kf[nt].y));
-                    const float2 al = make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y));
+                    l[nt] = fmul2(l[nt], make_float2(ex2(mn.x - m[nt].x), ex2(mn.y - m[nt].y)));
                     m[nt] = mn;
-                    thr[nt].x = mn.x == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.x) / kf[nt].x;
-                    thr[nt].y = mn.y == -kQ4NoMax ? -INFINITY : (kQ4Slack - mn.y) / kf[nt].y;
-                    l[nt] = fmul2(l[nt], al);
-                    const float2 f = make_float2(al.x * resc, al.y * resc);
 #pragma unroll
-                    for (int g = 0; g < G; ++g) zac[nt][g] = fmul2(zac[nt][g], f);
+                    for (int g = 0; g < G; ++g) {
+                        float2 w = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-                    for (int c = 0; c < MT; ++c) {
-                        acc[c][nt][0] = fmul2(acc[c][nt][0], f);
-                        acc[c][nt][1] = fmul2(acc[c][nt][1], f);
+                        for (int x = 0; x < NP; ++x)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const float s = __log2f(q4_step((y ? vm1 : vm0)[x][g]));       // (of 0 minus infinity)
+                                const float2 v = ffma2(sc[x][nt][y], kf[nt], make_float2(s, s));
+                                w.x = fmaxf(w.x, v.x);
+                                w.y = fmaxf(w.y, v.y);
+                            }
+                        w = largest(w);
+                        float2 &at = wmax[4 * (nt * G + g)], old = at;
+                        w.x = fmax3(old.x, w.x, -mn.x - kQ4Range);
+                        w.y = fmax3(old.y, w.y, -mn.y - kQ4Range);
+                        const float2 f = make_float2(ex2(old.x - w.x), ex2(old.y - w.y)), d = fadd2(w, mn);
+                        zac[nt][g] = fmul2(zac[nt][g], f);
+#pragma unroll
+                        for (int c = g * (MT / G); c < (g + 1) * (MT / G); ++c) {
+                            acc[c][nt][0] = fmul2(acc[c][nt][0], f);
+                            acc[c][nt][1] = fmul2(acc[c][nt][1], f);
+                        }
+                        __syncwarp();
+                        if (r8 == 0) {
+                            at = w;
+                            lim[4 * (nt * G + g)] = make_float2(d.x + kQ4Slack, d.y + kQ4Slack);
+                            beta[4 * (nt * G + g)] = make_float2(ex2(kQ4Top - d.x), ex2(kQ4Top - d.y));
+                        }
                     }
                 }
+                __syncwarp();
             }
 #pragma unroll
             for (int x = 0; x < NP; ++x) {
@@ -1253,12 +1302,14 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                 load_words<W>(vbase + at[x] * SB + 128 * W, v1);
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
-                    const float w0 = q4_step(vm0[x][g]) * beta, w1 = q4_step(vm1[x][g]) * beta;
+                    const float s0 = q4_step(vm0[x][g]), s1 = q4_step(vm1[x][g]);
                     const float z0 = q4_zero(vm0[x][g]), z1 = q4_zero(vm1[x][g]);
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        const float2 x0 = fmul2(p[nt][0], make_float2(w0, w0)), x1 = fmul2(p[nt][1], make_float2(w1, w1));
+                        const float2 bt = beta[4 * (nt * G + g)];
+                        const float2 x0 = fmul2(fmul2(p[nt][0], bt), make_float2(s0, s0));
+                        const float2 x1 = fmul2(fmul2(p[nt][1], bt), make_float2(s1, s1));
                         const uint32_t h0 = pack_f16(x0.x, x0.y), h1 = pack_f16(x1.x, x1.y);
                         zac[nt][g] = ffma2(f16_pair(h0), make_float2(z0, z0),
                                            ffma2(f16_pair(h1), make_float2(z1, z1), zac[nt][g]));

@@ -556,6 +556,11 @@ attn_status_t attn_kv_gather_paged_q4(
  *   workspace    >= attn_decode_q4_workspace_size(...) bytes, 16-byte aligned; its
  *                contents on entry do not matter.  Calls that could overlap on the
  *                GPU need one each.
+ *   precision    scores and sums in fp32; each weight p step is rounded to f16, by at most
+ *                2^-11 of itself or 2^-32 of its row's and group's largest, whichever is
+ *                more; p below 2^-126 of its row's largest counts as 0.  Elements of q below
+ *                2^-26 of their row's largest are rounded to multiples of 2^-33 of it, and
+ *                |q| is to be below 2^117.
  * Supported: head_dim in {64, 128}, Hq / Hkv <= 64, B <= 4096, any Hkv.
  */
 size_t attn_decode_q4_workspace_size(int B, int num_heads_q, int num_heads_kv, int head_dim);

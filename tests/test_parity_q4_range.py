@@ -230,3 +230,89 @@ def test_nan_group_leaves_the_other_groups(device, n, D, group, power, at):
     want = Attention(q, cache, L, group)
     assert torch.isnan(want.o[:, 4:, :group]).all() and int(torch.isnan(want.o).sum()) == n * 4 * group
     want.check(o[0], lse[0])
+
+
+# ---------------------------------------------------------------- steps far apart
+@gpu
+@pytest.mark.parametrize("power", [20, 24, 30, 60, -60])
+@pytest.mark.parametrize("n,window", [(1, 300), (1, 0), (3, 100)])
+def test_hidden_key_of_another_size(device, power, n, window):
+    """A key outside the window, on a page that the window's first keys share, changes nothing."""
+    L, Hkv, D, group = 1000, 1, 128, 64
+    k, v = randn((L, Hkv, D), 20), randn((L, Hkv, D), 21)
+    first = L - n - window                               # the window's first key; its page holds earlier ones
+    assert first % 16
+    cache = cache_of(k, v, group)
+    v[first - 1] = (v[first - 1].float() * 2.0 ** power).to(torch.bfloat16)
+    big = cache_of(k, v, group)
+    q = randn((n, 4, D), 22)
+    o, lse = attend([q], [big], [L], group, window=window)
+    want = Attention(q, cache, L, group, window=window)
+    want.check(o[0], lse[0])
+
+
+@gpu
+@pytest.mark.parametrize("power", [24, 30, 60])
+def test_key_that_causality_hides(device, power):
+    """The newest key's values reach the newest query alone."""
+    L, Hkv, D, group, n = 700, 1, 64, 32, 3
+    k, v = randn((L, Hkv, D), 23), randn((L, Hkv, D), 24)
+    v[-1] = (v[-1].float() * 2.0 ** power).to(torch.bfloat16)
+    run(randn((n, 4, D), 25), k, v, group)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("power,below", [(20, 30), (24, 40), (30, 25), (30, 30), (30, 45), (60, 80), (60, 60), (100, 99)])
+@pytest.mark.parametrize("at", [0, 555, 999])
+def test_strong_key_of_little_weight(device, n, power, below, at):
+    """Values 2^power times the others' on a key whose p is 2^-below of theirs."""
+    L, Hkv, D, group = 1000, 1, 128, 32
+    k, v = randn((L, Hkv, D), 26, 0.05), randn((L, Hkv, D), 27)
+    q = randn((n, 2, D), 28)
+    away = -q[0, 0].double()                             # every query shares head 0's direction
+    q[:] = q[0, 0]
+    t = below * math.log(2) * math.sqrt(D) / float(away @ away)
+    k[at] = (away * t).to(torch.bfloat16)
+    v[at] = (v[at].float() * 2.0 ** power).to(torch.bfloat16)
+    run(q, k, v, group, causal=False if n > 1 else True)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("powers", [(0, 30, -30, 60), (40, 0, 0, -90), (-20, 17, 0, 8)])
+def test_groups_of_different_size(device, n, powers):
+    """Each group's columns are as exact as if the others were not there."""
+    L, D, group = 600, 128, 32
+    v = randn((L, 1, D), 29).float().unflatten(-1, (4, 32)) * torch.tensor([2.0 ** p for p in powers])[:, None]
+    run(randn((n, 4, D), 30), randn((L, 1, D), 31), v.flatten(-2).to(torch.bfloat16), group)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("order", [1, -1])
+def test_sizes_that_grow_along_the_sequence(device, n, order):
+    L, D, group = 1500, 64, 32
+    size = torch.linspace(-40, 40, L).round()[:, None, None] * order
+    v = (randn((L, 1, D), 32).float() * 2.0 ** size).to(torch.bfloat16)
+    run(randn((n, 4, D), 33), randn((L, 1, D), 34), v, group)
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+def test_groups_of_zeros_and_a_sharp_key(device, n):
+    """Values of zero everywhere but on keys of little weight, and a key that takes all of it."""
+    L, D, group = 800, 64, 32
+    v = torch.zeros(L, 1, D, dtype=torch.bfloat16)
+    v[10] = randn((1, D), 35)
+    v[500, 0, 32:] = randn((32,), 36, 2.0 ** -90)
+    k = randn((L, 1, D), 37)
+    q = randn((n, 2, D), 38)
+    run(q, k, v, group)
+    q[:] = q[0, 0]
+    k[600] = (q[0, 0].float() * 1.5).to(torch.bfloat16)      # about 2^17 of the others; its values are zero
+    run(q, k, v, group)
+    k[600] = (q[0, 0].float() * 30).to(torch.bfloat16)       # past 2^-126: the others' p are zero
+    cache = cache_of(k, v, group)
+    o, _ = attend([q], [cache], [L], group)
+    assert not o[0][-1].any()
