@@ -1208,6 +1208,18 @@ __global__ void __launch_bounds__(32 * (q4_warps(NT) + kQ4Producers), 1) q4_attn
                                 if (key > last || key >= L || (a.window >= 0 && key < last - a.window))
                                     (e ? sc[x][nt][y].y : sc[x][nt][y].x) = -INFINITY;
                             }
+                        // A NaN step reaches the rows that see its key, by way of the sums, and no weight of 0.
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            uint32_t& meta = (y ? vm1 : vm0)[x][g];
+                            if ((meta & 0x7f80u) != 0x7f80u) continue;
+                            meta = 0;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (sc[x][nt][y].x != -INFINITY) zac[nt][g].x = NAN;
+                                if (sc[x][nt][y].y != -INFINITY) zac[nt][g].y = NAN;
+                            }
+                        }
                     }
             }
             // Does a score exceed its row's maximum by the slack, or a weight its own?  (Of the weights a

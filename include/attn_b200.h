@@ -581,6 +581,9 @@ attn_status_t attn_decode_paged_q4(
  *   workspace    >= attn_fwd_q4_workspace_size(...) bytes, 16-byte aligned; as above.
  * Up to 128 query rows per KV head (max_seqlen_q * Hq / Hkv) attend to the 4-bit
  * pages as they are; more, to bf16 rows that the call reads back first.
+ * A NaN among a token's values reaches the queries that see the token; on the rows that
+ * are read back it may also reach queries of the same sequence from which the mask
+ * hides the token.
  */
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int num_heads_q, int num_heads_kv,
                                   int head_dim, int total_k);

@@ -316,3 +316,35 @@ def test_groups_of_zeros_and_a_sharp_key(device, n):
     cache = cache_of(k, v, group)
     o, _ = attend([q], [cache], [L], group)
     assert not o[0][-1].any()
+
+
+@gpu
+@pytest.mark.parametrize("n,window", [(1, 300), (1, 0), (3, 100)])
+def test_nan_before_the_window(device, n, window):
+    L, D, group = 1000, 64, 32
+    first = L - n - window
+    k, v = randn((L, 1, D), 40), randn((L, 1, D), 41)
+    q = randn((n, 4, D), 42)
+    cache = cache_of(k, v, group)
+    want = Attention(q, cache, L, group, window=window)
+    for m in cache[2:]:
+        m[(first - 1) // 16, 0, (first - 1) % 16] = 0x7FC0
+    o, lse = attend([q], [cache], [L], group, window=window)
+    want.check(o[0], lse[0])
+
+
+@gpu
+@pytest.mark.parametrize("n", [2, 3, 8, 20])
+def test_nan_that_causality_hides(device, n):
+    """NaN values of a drafted token reach the queries from it on, and no earlier one."""
+    L, D, group = 500, 64, 32
+    cache = cache_of(randn((L, 2, D), 43), randn((L, 2, D), 44), group)
+    q = randn((n, 4, D), 45)
+    t = L - n + n // 2                                       # the token of query n // 2
+    cache[3][t // 16, 0, t % 16, 1] = 0x7FC0                 # its values of head 0, second group
+    cache[2][t // 16, 1, t % 16, 0] = 0x7FC0                 # its key of head 1
+    o, lse = attend([q], [cache], [L], group)
+    want = Attention(q, cache, L, group)
+    assert int(torch.isnan(want.o[:, :2]).sum()) == (n - n // 2) * 2 * 32
+    assert torch.isnan(want.o[n // 2:, 2:]).all() and not torch.isnan(want.o[:n // 2]).any()
+    want.check(o[0], lse[0])
