@@ -322,7 +322,10 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     if (threadIdx.x < 32) {
-        int run_p = 0, run_r = 0;
+        // (rows are held at 2^31 - 1, past any output: the lengths' sum may be more)
+        constexpr uint32_t kMost = 0x7fffffffu;
+        int run_p = 0;
+        uint32_t run_r = 0;
         for (int base = 0; base < a.B; base += 32) {
             const int b = base + lane;
             int n = 0, np = 0, s0 = 0;
@@ -332,22 +335,25 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
                 n = min(max(n, 0), max(a.max_blocks * kPageRows - s0, 0));
                 np = n > 0 ? (s0 + n - 1) / kPageRows - s0 / kPageRows + 1 : 0;
             }
-            int ip = np, ir = n;
+            int ip = np;
+            uint32_t ir = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, ip, o), y = __shfl_up_sync(0xffffffffu, ir, o);
-                if (lane >= o) ip += x, ir += y;
+                const int x = __shfl_up_sync(0xffffffffu, ip, o);
+                const uint32_t y = __shfl_up_sync(0xffffffffu, ir, o);
+                if (lane >= o) ip += x, ir = min(ir + y, kMost);
             }
+            const uint32_t before = __shfl_up_sync(0xffffffffu, ir, 1);
             if (b < a.B) {
                 pages[b] = run_p + ip - np;
-                rows[b] = a.cu ? a.cu[b] : run_r + ir - n;
+                rows[b] = a.cu ? a.cu[b] : (int)min(run_r + (lane ? before : 0u), kMost);
             }
             run_p += __shfl_sync(0xffffffffu, ip, 31);
-            run_r += __shfl_sync(0xffffffffu, ir, 31);
+            run_r = min(run_r + __shfl_sync(0xffffffffu, ir, 31), kMost);
         }
         if (lane == 0) {
             pages[a.B] = run_p;
-            rows[a.B] = a.cu ? a.cu[a.B] : run_r;
+            rows[a.B] = a.cu ? a.cu[a.B] : (int)run_r;
             if (blockIdx.x == 0 && rows[a.B] > a.total) record_data_error(kErrQ4Rows);
         }
     }
@@ -382,6 +388,8 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
         const Item x = next;
         if (it + warps < items) next = look_up(it + warps);      // in flight beside this one
         const int h = x.h, b = x.b, s0 = x.s0, slot = x.slot, n = x.n;
+        // (all further rows lie behind the output's last: lengths past `total` cost no time)
+        if (!a.cu && (long long)rows[b] + slot * kPageRows >= a.total) break;
         int page = x.page;
         if (page < 0 || page >= a.num_blocks) {
             if (lane == 0) record_data_error(kErrDecPageRange);

@@ -1,0 +1,65 @@
+"""attn_fwd_varlen_paged_q4 past the page stream with a total_k that the lengths exceed: reported,
+the keys that fit read back, nothing outside the workspace written."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from attention_paged_kv_gqa_b200 import binding as A
+from oracle import rope_q4 as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TOL_O, TOL_LSE = 2e-2, 1e-3              # the tensor-core forward's elsewhere (probabilities in bf16)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    assert A.attn_check_device(0) == 0
+    torch.cuda.set_device(0)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def randn(shape, seed):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+
+
+class Space:
+    """A workspace of exactly the size that is asked for, between bytes that must stay."""
+
+    def __init__(self, need):
+        self.all = torch.full((need + 8192,), 0xA5, dtype=torch.uint8, device=DEV)
+        self.ws = self.all[4096:4096 + need]
+
+    def untouched(self):
+        return bool((self.all[:4096] == 0xA5).all()) and bool((self.all[4096 + self.ws.numel():] == 0xA5).all())
+
+
+def test_sum_of_lengths_past_31_bits():
+    """Lengths whose sum is past 2^31 are seen to exceed total_k; the rows' offsets stay within it."""
+    B, Hq, Hkv, D, group, total_k, n = 5, 2, 1, 64, 32, 50, 70
+    cache = R.fill((1, Hkv, 16, D // 2), group, 1)
+    bt = torch.zeros(B, 1 << 25, dtype=torch.int32, device=DEV)          # (every page is page 0)
+    q = randn((n + 4, Hq, D), 2)
+    need = A.attn_fwd_q4_workspace_size(B, n, Hq, Hkv, D, total_k)
+    space = Space(need)
+    o, lse = A.attn_fwd_varlen_paged_q4(q.to(DEV), *(t.to(DEV) for t in cache), block_table=bt,
+                                        cu_seqlens_q=i32([0, n, n + 1, n + 2, n + 3, n + 4]).to(DEV), max_seqlen_q=n,
+                                        seqused_k=i32([1 << 29] * B).to(DEV), total_k=total_k, mask=A.MASK_NONE,
+                                        workspace=space.ws)
+    assert A.attn_device_error() == 531
+    assert space.untouched()
+    rows = 2 * total_k * Hkv * D * 2
+    assert space.ws[rows:rows + 4 * (B + 1)].view(torch.int32).tolist() == [0] + [total_k] * B
+    # the first sequence's keys that fit: tokens 0 .. 49; the others have none
+    k, v = R.packed(*cache, torch.zeros(1, 4, dtype=torch.int32), [total_k])
+    o_ref, lse_ref = oracle.attn_varlen(q[:n], k, v, cu_seqlens_q=[0, n], cu_seqlens_k=[0, total_k], num_heads_kv=Hkv,
+                                        scale=D ** -0.5, mask=0)
+    assert np.abs(o[:n].double().cpu().numpy() - o_ref).max() <= TOL_O
+    assert np.abs(lse[:, :n].double().cpu().numpy() - lse_ref).max() <= TOL_LSE
+    assert not o[n:].any() and bool(torch.isneginf(lse[:, n:]).all())
