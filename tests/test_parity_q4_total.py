@@ -63,3 +63,27 @@ def test_sum_of_lengths_past_31_bits():
     assert np.abs(o[:n].double().cpu().numpy() - o_ref).max() <= TOL_O
     assert np.abs(lse[:, :n].double().cpu().numpy() - lse_ref).max() <= TOL_LSE
     assert not o[n:].any() and bool(torch.isneginf(lse[:, n:]).all())
+
+
+@pytest.mark.parametrize("total_k", [120, 100, 133])
+def test_first_sequences_and_the_bytes_behind_the_workspace(total_k):
+    Hq, Hkv, D, group, lens, qs = 4, 2, 64, 32, [100, 34], [10, 70]
+    need = [(m + 15) // 16 for m in lens]
+    bt = torch.full((2, max(need)), 1 << 29, dtype=torch.int32)
+    bt[0, :need[0]], bt[1, :need[1]] = torch.arange(need[0]) + 1, torch.arange(need[1]) + 1 + need[0]
+    cache = R.fill((sum(need) + 1, Hkv, 16, D // 2), group, 33)
+    q = randn((80, Hq, D), 34)
+    space = Space(A.attn_fwd_q4_workspace_size(2, 70, Hq, Hkv, D, total_k))
+    o, lse = A.attn_fwd_varlen_paged_q4(q.to(DEV), *(t.to(DEV) for t in cache), block_table=bt.to(DEV),
+                                        cu_seqlens_q=i32([0, 10, 80]).to(DEV), max_seqlen_q=70, seqused_k=i32(lens).to(DEV),
+                                        total_k=total_k, mask=A.MASK_CAUSAL, workspace=space.ws)
+    assert A.attn_device_error() == 531
+    assert space.untouched()
+    k, v = R.packed(*cache, bt, [100, total_k - 100])
+    assert torch.equal(space.ws[:k.numel() * 2].view(torch.bfloat16).cpu(), k.flatten())
+    assert torch.equal(space.ws[k.numel() * 2:k.numel() * 4].view(torch.bfloat16).cpu(), v.flatten())
+    o_ref, lse_ref = oracle.attn_varlen(q[:10], k[:100], v[:100], cu_seqlens_q=[0, 10], cu_seqlens_k=[0, 100],
+                                        num_heads_kv=Hkv, scale=D ** -0.5, mask=1)
+    assert np.abs(o[:10].double().cpu().numpy() - o_ref).max() <= TOL_O
+    assert np.abs(lse[:, :10].double().cpu().numpy() - lse_ref).max() <= TOL_LSE
+    assert torch.isfinite(o).all()
