@@ -348,3 +348,66 @@ def test_nan_that_causality_hides(device, n):
     assert int(torch.isnan(want.o[:, :2]).sum()) == (n - n // 2) * 2 * 32
     assert torch.isnan(want.o[n // 2:, 2:]).all() and not torch.isnan(want.o[:n // 2]).any()
     want.check(o[0], lse[0])
+
+
+# ---------------------------------------------------------------- long sequences
+LONG = [(9000, 4, 1, 128, 128), (30011, 2, 1, 128, 32), (65003, 2, 1, 64, 64), (4100, 8, 4, 128, 64)]
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3, 20])
+@pytest.mark.parametrize("L,Hq,Hkv,D,group", LONG)
+def test_long_sequences(device, L, Hq, Hkv, D, group, n):
+    run(randn((n, Hq, D), 50), randn((L, Hkv, D), 51), randn((L, Hkv, D), 52), group)
+
+
+@pytest.mark.parametrize("L,Hq,Hkv,D,group", LONG)
+@pytest.mark.parametrize("page", [0.0, 0.3, 1.0])
+def test_a_page_left_out_would_be_seen(L, Hq, Hkv, D, group, page):
+    """The tolerances refuse attention over all pages but one, in fp64, by its LSE and by its O."""
+    q, k, v = randn((1, Hq, D), 50), randn((L, Hkv, D), 51), randn((L, Hkv, D), 52)
+    cache = cache_of(k, v, group)
+    want = Attention(q, cache, L, group)
+    at = int(page * (-(-L // 16) - 1)) * 16
+    less = Attention(q, cache, L, group, skip=[(at, at + 16)])
+    eo, el = want.excess(less.o.to(torch.bfloat16), less.lse)
+    assert el > 1, el
+    assert eo > 1, eo
+    assert max(want.excess(want.o.to(torch.bfloat16), want.lse)) <= 0.95
+
+
+@gpu
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("L,Hkv,group", [(60000, 1, 64), (777, 2, 32)])
+def test_every_page_counts(device, L, Hkv, group, n):
+    """One page in turn holds the one key that matters: its values are the output."""
+    D = 64
+    k, v = randn((L, Hkv, D), 53), randn((L, Hkv, D), 54)
+    q = randn((n, Hkv, D), 55)
+    q[:] = q[0]
+    cache = cache_of(k, v, group)
+    strong = (q[0].float() * 6).to(torch.bfloat16)
+    values = torch.from_numpy(R.read(cache[1], cache[3], list(range(-(-L // 16))), False))
+    kc, km = pages_of(strong[None], group, R.k_nibble)
+    pages = range(-(-L // 16)) if L < 1000 else range(0, L // 16, 97)
+    dc, bt = [t.to(DEV) for t in cache], torch.arange(-(-L // 16), dtype=torch.int32)[None].to(DEV)
+    dq, dl, cu = q.to(DEV), i32([L]).to(DEV), i32([0, n]).to(DEV)
+    for p in pages:
+        t = p * 16 + p % 16
+        if t > L - n:
+            continue
+        keep = [dc[0][p].clone(), dc[2][p].clone()]
+        dc[0][p, :, p % 16] = kc[0, :, 0].to(DEV)
+        dc[2][p, :, p % 16] = km[0, :, 0].to(DEV)
+        if n == 1:
+            o, _ = A.attn_decode_paged_q4(dq, *dc, bt, dl)
+        else:
+            o, _ = A.attn_fwd_varlen_paged_q4(dq, *dc, block_table=bt, cu_seqlens_q=cu, max_seqlen_q=n, seqused_k=dl,
+                                              total_k=L, mask=A.MASK_CAUSAL)
+        dc[0][p], dc[2][p] = keep
+        # 6 |q|^2 / 8 is 40 or more above the other scores (of deviation 1, or |q| = 8): they weigh
+        # 60000 e^-30 at most
+        o = o.double().cpu()
+        err = (o - values[t]).abs() - 2.0 ** -8 * values[t].abs()
+        assert float(err.max()) <= 2.0 ** -10 * float(values[t].abs().max()), (p, float(err.max()))
+    assert A.attn_device_error() == 0
