@@ -173,13 +173,15 @@ attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, s
 
 template <int D, int GS>
 attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
-    // A page and head per warp.  Every block builds the tables: that is cheap for up to 16
-    // sequences, and a block then takes eight (8 sequences of 16000 tokens 111 us, with two
-    // lasting blocks to an SM 127; 16 of 3688: 55.5 and 60.5; 16 of 300: 11.3 and 12.3).  For
-    // more sequences two lasting blocks to an SM (32 of 500: 18.4 us, in eights 20.4; 512 of 100:
-    // 59 and 90; with three 61, with four 73).
+    // A page and head per warp.  Every block builds the tables, which is cheap for up to 64
+    // sequences: then sixteen blocks to an SM, of which four are there at once and the next follows
+    // where one ends (8 sequences of 16000 tokens 112 us, with two lasting blocks to an SM 125; 24
+    // of 4000 86 and 94; 64 of 4000 222 and 244; 32 of 500 19 and 18), and no more, since `total`
+    // may be far above the rows there are (8 of 500 under a total 64 times theirs, forward included:
+    // 30.7 us, with a block for each eight pages of the total 56).  For more sequences two lasting
+    // blocks (128 of 2000: 243 us, with a block for each eight pages 244; 512 of 100: 59 and 90).
     const long long items = ((long long)a.total / kPageRows + 2LL * a.B) * a.Hkv, blocks = (items + 7) / 8;
-    const int grid = (int)std::max<long long>(1, std::min<long long>(blocks, a.B <= 16 ? INT_MAX : (long long)sms * 2));
+    const int grid = (int)std::max<long long>(1, std::min<long long>(blocks, (long long)sms * (a.B <= 64 ? 16 : 2)));
     q4_gather_kernel<D, GS><<<grid, 256, 2 * (a.B + 1) * sizeof(int), st>>>(a);
     return launch_status();
 }

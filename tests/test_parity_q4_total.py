@@ -1,5 +1,6 @@
-"""attn_fwd_varlen_paged_q4 past the page stream with a total_k that the lengths exceed: reported,
-the keys that fit read back, nothing outside the workspace written."""
+"""attn_fwd_varlen_paged_q4 past the page stream with a total_k that the lengths exceed (reported,
+the keys that fit read back, nothing outside the workspace written) or stay far below, and the
+read-back of more pages than its blocks take at once."""
 import numpy as np
 import pytest
 import torch
@@ -87,3 +88,36 @@ def test_first_sequences_and_the_bytes_behind_the_workspace(total_k):
     assert np.abs(o[:10].double().cpu().numpy() - o_ref).max() <= TOL_O
     assert np.abs(lse[:, :10].double().cpu().numpy() - lse_ref).max() <= TOL_LSE
     assert torch.isfinite(o).all()
+
+
+def test_total_far_above_the_lengths():
+    Hq, Hkv, D, group, lens = 4, 2, 64, 32, [100, 0, 34]
+    n = [(m + 15) // 16 for m in lens]
+    bt = torch.zeros(3, max(n), dtype=torch.int32)
+    bt[0, :n[0]], bt[2, :n[2]] = torch.arange(n[0]) + 1, torch.arange(n[2]) + 1 + n[0]
+    cache = [t.to(DEV) for t in R.fill((sum(n) + 1, Hkv, 16, D // 2), group, 35)]
+    q, cu = randn((81, Hq, D), 36).to(DEV), i32([0, 10, 11, 81]).to(DEV)
+    got = []
+    for total_k in (134, 2_000_000):
+        space = Space(A.attn_fwd_q4_workspace_size(3, 70, Hq, Hkv, D, total_k))
+        got.append(A.attn_fwd_varlen_paged_q4(q, *cache, block_table=bt.to(DEV), cu_seqlens_q=cu, max_seqlen_q=70,
+                                              seqused_k=i32(lens).to(DEV), total_k=total_k, mask=A.MASK_CAUSAL,
+                                              workspace=space.ws))
+        assert A.attn_device_error() == 0 and space.untouched()
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("lens", [[40001], [700] * 64, [300] * 65, [0, 33, 20000, 1, 16, 19000]])
+def test_read_back_of_many_pages(lens):
+    Hkv, D, group = 8, 64, 32
+    n = [(m + 15) // 16 for m in lens]
+    order = torch.randperm(sum(n), generator=torch.Generator().manual_seed(37)).to(torch.int32)
+    bt = torch.full((len(lens), max(n)), 1 << 29, dtype=torch.int32)
+    for b, pages in enumerate(order.split(n)):
+        bt[b, :n[b]] = pages
+    cache = R.fill((sum(n), Hkv, 16, D // 2), group, 38)
+    cu = i32(np.concatenate([[0], np.cumsum(lens)]))
+    gk, gv = A.attn_kv_gather_paged_q4(*(t.to(DEV) for t in cache), bt.to(DEV), cu.to(DEV), int(cu[-1]))
+    assert A.attn_device_error() == 0
+    k, v = R.packed(*cache, bt, lens)
+    assert torch.equal(gk.cpu(), k) and torch.equal(gv.cpu(), v)
