@@ -14,6 +14,18 @@ bool stride8(const int64_t* s, int n) {
     return true;
 }
 
+// Do the heads of an output with these {token, head} strides lie apart: a token's all before the
+// next token's, or a head's tokens all before the next head's?
+bool own_places(const int64_t* s, int total, int H, int D) {
+    auto within = [D](int64_t outer, int64_t inner, int n) { return n <= 1 || (outer - D) / (n - 1) >= inner; };
+    return s[0] >= D && s[1] >= D && (within(s[0], s[1], H) || within(s[1], s[0], total));
+}
+
+// Strides of the same layout, where there is more than one token and head.
+bool same_places(const int64_t* a, const int64_t* b, int total, int H) {
+    return (total <= 1 || a[0] == b[0]) && (H <= 1 || a[1] == b[1]);
+}
+
 // Arguments of the table: cos_sin null means no rotation (where `optional`).
 attn_status_t check_rope(const float* cos_sin, int max_position, int rot_dim, const int32_t* positions, int n_axes,
                          const int32_t* pair_axis, int D, bool optional) {
@@ -252,8 +264,11 @@ attn_status_t attn_rope(const void* q, void* q_out, const void* k, void* k_out, 
         return ATTN_ERR_INVALID_ARG;
     if (k && (!aligned16(k) || !aligned16(k_out) || !stride8(strides_k, 2) || !stride8(strides_k_out, 2)))
         return ATTN_ERR_INVALID_ARG;
-    for (int i = 0; i < 2; ++i)        // outputs: every head its own place
-        if (strides_q_out[i] < D || (k && strides_k_out[i] < D)) return ATTN_ERR_INVALID_ARG;
+    if (!own_places(strides_q_out, total, Hq, D) || (k && !own_places(strides_k_out, total, Hkv, D)))
+        return ATTN_ERR_INVALID_ARG;
+    if ((q == q_out && !same_places(strides_q, strides_q_out, total, Hq)) ||
+        (k && k == k_out && !same_places(strides_k, strides_k_out, total, Hkv)))
+        return ATTN_ERR_INVALID_ARG;
     int dev = 0;
     if ((s = current_device_ok(&dev)) != ATTN_OK) return s;
     if (total == 0) return ATTN_OK;

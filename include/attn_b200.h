@@ -452,8 +452,10 @@ attn_status_t attn_decode_paged_noalloc(
  *   q [total, Hq, D], k [total, Hkv, D] (NULL with Hkv 0: q alone) bf16, element
  *                  strides {token, head} given per tensor (multiples of 8: views
  *                  of a packed QKV tensor are taken as they are).
- *   q_out, k_out   as q and k, with strides of at least head_dim; either the input
- *                  itself (in place) or memory that no input shares.
+ *   q_out, k_out   as q and k, with strides of at least head_dim by which a token's heads
+ *                  all lie before the next token's, or a head's tokens all before the
+ *                  next head's; either the input itself, with its strides (in place), or
+ *                  memory that no input shares.
  *   cos_sin        fp32 [max_position, rot_dim], 16-byte aligned.
  *   positions      int32 [n_axes, total].
  *   pair_axis      int32 [rot_dim / 2], 16-byte aligned: the axis of each pair
