@@ -74,16 +74,17 @@ constexpr int kQ4Few = 32 * kQ4Scan;
 constexpr int kQ4Smem = 227 * 1024 - 256;      // (some is static)
 
 // Eights of query rows that a warp holds.  Up to eight rows: one, which at 128 registers leaves
-// room for twelve warps, and those hide each other's waits best (3 sequences of 65000 keys 72
-// us, with eight warps 75).  More: two, so that half as many warps take the codes of a page
-// apart; they need 168 registers, eight warps (16 sequences of 3700 keys, groups of four: 8
-// queries 70 us, one eight to each of eight warps 81, of twelve 84; 16 queries 119, 148, 156).
+// room for twelve warps, and those hide each other's waits best (3 sequences of 65000 keys 77
+// us, with eight warps 79; 32 of 4100 46 and 48).  More: two, so that half as many warps take
+// the codes of a page apart; they need 168 registers, eight warps (16 sequences of 3700 keys,
+// groups of four: 8 queries 73 us, one eight to each of eight warps 85, of twelve 91; 16 queries
+// 126, 155, 155).
 int q4_tile(int rows) { return rows <= 8 ? 1 : 2; }
 
 // Row tiles of a KV head, KV heads of a CTA's block, and warps of a head and row tile: the
 // block with the most of the CTA's warps at work, the largest such one (its copies are
 // longest), but of two eights to a warp at most four heads: with eight, whose queries take
-// twice as long to prepare, 4 queries take 47 us in place of 43 (with two 48).
+// twice as long to prepare, 4 queries take 50 us in place of 44 (with two 49).
 void q4_split(int Hkv, int rows, int* RT, int* HB, int* SUB) {
     const int NT = q4_tile(rows), warps = q4_warps(NT);
     *RT = (rows + 8 * NT - 1) / (8 * NT);
@@ -105,9 +106,9 @@ int sm_count_or_most() {
 }
 
 // The combine kernel takes the shares of more than kQ4Few sequences from a table that the
-// attention kernel leaves behind the partials (600 sequences of 100 keys: 109 us without it,
-// 89 with), those of fewer from the lengths, while the attention kernel still runs (32
-// sequences of 4100 keys: 45.2 us, with the table 46.1).
+// attention kernel leaves behind the partials (600 sequences of 100 keys: 106 us without it,
+// 90 with), those of fewer from the lengths, while the attention kernel still runs (32
+// sequences of 4100 keys, calls in a row: 40.1 us, with the table 40.8).
 size_t q4_table_bytes(int B) { return B > kQ4Few ? 8 + (size_t)(B + 1) * sizeof(int2) : 0; }
 
 size_t q4_workspace(int B, int Hkv, int D, int rows, int sms) {
@@ -186,7 +187,7 @@ attn_status_t launch_q4(const Q4AttnArgs& a, int D, int GS, int sms, void* ws, s
 template <int D, int GS>
 attn_status_t launch_q4_gather_t(const Q4GatherArgs& a, int sms, cudaStream_t st) {
     // A page and head per warp.  Every block builds the tables, which is cheap for up to 64
-    // sequences: then sixteen blocks to an SM, of which four are there at once and the next follows
+    // sequences: then sixteen blocks to an SM, of which three are there at once and the next follows
     // where one ends (8 sequences of 16000 tokens 112 us, with two lasting blocks to an SM 125; 24
     // of 4000 86 and 94; 64 of 4000 222 and 244; 32 of 500 19 and 18), and no more, since `total`
     // may be far above the rows there are (8 of 500 under a total 64 times theirs, forward included:
@@ -493,9 +494,9 @@ attn_status_t attn_decode_paged_q4(const void* q, const void* k_cache, const voi
 }
 
 // The page stream serves up to 128 query rows per KV head; above that the pages are read back
-// as packed bf16 rows (exact) and the tensor-core forward runs on those.  (Groups of four, 16
-// sequences of 3700 keys: 17 to 32 queries 210 to 217 us, read back 228; 2 sequences of 40000:
-// 281 to 286 us, read back 847.)
+// as packed bf16 rows (exact) and the tensor-core forward runs on those.  (Groups of four, 2
+// sequences of 40000 keys: 24 and 32 queries 300 and 304 us, read back 843; 16 sequences of 3700:
+// 17 to 32 queries 222 to 232 us, read back 220; 16 queries 126 and 220.)
 static bool q4_fwd_streams(int max_seqlen_q, int group) { return (long long)max_seqlen_q * group <= kQ4Rows; }
 
 size_t attn_fwd_q4_workspace_size(int B, int max_seqlen_q, int Hq, int Hkv, int D, int total_k) {

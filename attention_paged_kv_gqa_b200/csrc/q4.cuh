@@ -490,22 +490,27 @@ __global__ void __launch_bounds__(256) q4_gather_kernel(const Q4GatherArgs a) {
 // The first sum is far larger than the difference where p is spread over many
 // keys, and the tensor cores truncate when they add; every 16 pages the second
 // sum is therefore taken out of the accumulators, which stay near their final size
-// (every 4 or every 64 pages take the same time).  The running maximum moves only
-// when a score exceeds it by 2^8, which a page shows by one vote (48.6 us on the
-// first case below if it moves with every larger score, against 47).
+// (every 4 or every 64 pages take the same time, within 2 %).  The running maximum of
+// the scores, and that of the weights, moves only when one exceeds it by 2^8, which a
+// page shows by one vote (the second case below takes 91 us if they move with every
+// larger one, against 77).
 //
 // Bound.  Bytes would take 20 us for 32 sequences of 4100 keys (32 + 8 heads of 128, groups
-// of 128) and 35 us for 3 of 65000 (64 + 8, groups of 32); the calls take 43 to 46 and 70 to
-// 73.  About 14 us are fixed: 4 to 5 until the first page is there (launch, lengths, table,
-// page), 1.5 to 2 for the join, 4 to 6 for the combine kernel.  A page of four heads then
-// costs 0.27 us of a CTA's time, where its bytes take 0.20: taking the codes apart keeps the
-// logic pipe at 51 and 61 % of its rate over the whole call, and the chain from score to
-// weight does not leave it busy throughout.  The tensor pipe is at 20 %, DRAM at half.  A
-// change of sequence costs 3 to 4 us (kQ4Switch: with 0, 6 and 20 in place of 13 the first
-// case took 51, 49 and 47 us against 47, 600 sequences of 100 keys 149, 123 and 113 against 114).
+// of 128) and 35 us for 3 of 65000 (64 + 8, groups of 32).  With cold caches, as are all
+// figures here that do not say otherwise, the calls take 45 to 46 and 76 to 79 us; in a row,
+// each beginning while the one before ends, 39 and 70.  About 14 us are fixed: 4 to 5 until
+// the first page is there (launch, lengths, table, page), 1.5 to 2 for the join, 4 to 6 for
+// the combine kernel.  A page of four heads then costs 0.26 us of a CTA's time, where its
+// bytes take 0.19: taking the codes apart keeps the logic pipe at 49 and 57 % of its rate
+// over the whole call, and the chain from score to weight does not leave it busy throughout.
+// The tensor pipe is at 21 and 18 %, DRAM at half.  The scales per row and group cost the
+// second case 2 us, the sum of the zeros over rounded weights another 2 (each 1 or less in
+// the first case).  A change of sequence costs 3 to 4 us (kQ4Switch: with 0, 6 and 20 in
+// place of 13 the first case takes 50, 48 and 46 us against 46, 600 sequences of 100 keys
+// 118, 97 and 88 against 90).
 // Tried and slower: MMAs on e4m3 codes (the warp form is emulated: 1.6 times), shifts on the
 // multiplier, the next pages' scores ahead of this pair's softmax (with twelve warps 49 us
-// against 45).
+// against 45, at the time).
 constexpr float kQ4Slack = 8.0f;         // p <= 2^8 between moves of the maximum, and w <= 2^8 of its own
 constexpr float kQ4Top = 7.0f;           // the largest w seen is 2^7 (one of 2^15 still fits)
 constexpr float kQ4Range = 111.0f;       // w's maximum is held at 2^-111 of p's or more: p scale <= 2^126
@@ -523,7 +528,7 @@ struct Q4AttnArgs {
     int HB, RT, SUB, nhb;    // KV heads of a block, row tiles, warps of a head and tile, blocks
     const __nv_bfloat16* q;  // rows of queries [..][Hq][D]
     const int* cu_q;         // [B + 1], or null: one query per sequence
-    int max_q;               // query tokens a sequence may have (group * max_q <= 8 RT)
+    int max_q;               // query tokens a sequence may have (group * max_q <= 8 NT RT)
     int total_q;
     int total_k;             // < 0, or what the caller takes the lengths' sum to be at most
     const uint8_t *k_cache, *v_cache;

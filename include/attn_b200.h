@@ -523,6 +523,10 @@ attn_status_t attn_kv_append_rope_paged(
  * run; of token 8 a + 2 c + h, dim 32 u + 8 j + r is nibble j of the 16-bit piece
  * (((8 a + r) 4 + c) W + u) 2 + h.
  * The cache format is this library's own; no page describes one below 8 bits.
+ * The calls on it take at most 4096 sequences, fewer than 2^31 entries of the block table
+ * (the attention: fewer than 2^31 / Hkv, each sequence counted as 13 more), fewer than
+ * 2^31 tokens of the cache and 2^30 of a sequence, head_dim in {64, 128}; else they
+ * return ATTN_ERR_UNSUPPORTED.
  */
 
 /*
@@ -563,7 +567,7 @@ attn_status_t attn_kv_gather_paged_q4(
  *                more; p below 2^-126 of its row's largest counts as 0.  Elements of q below
  *                2^-26 of their row's largest are rounded to multiples of 2^-33 of it, and
  *                |q| is to be below 2^117.
- * Supported: head_dim in {64, 128}, Hq / Hkv <= 64, B <= 4096, any Hkv.
+ * Supported: Hq / Hkv <= 64, any Hkv.
  */
 size_t attn_decode_q4_workspace_size(int B, int num_heads_q, int num_heads_kv, int head_dim);
 attn_status_t attn_decode_paged_q4(
