@@ -449,18 +449,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return r;
 }
 
-// The two halves of an f16x2 in fp32 (exact).
-__device__ __forceinline__ float2 f16_pair(uint32_t x) {
-    float2 r;
-    asm("{\n\t.reg .b16 lo, hi;\n\t"
-        "mov.b32 {lo, hi}, %2;\n\t"
-        "cvt.f32.f16 %0, lo;\n\t"
-        "cvt.f32.f16 %1, hi;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "r"(x));
-    return r;
-}
-
 // D(16x8 f32) += A(16x16 f16, row) * B(16x8 f16, col)
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1) {

@@ -583,6 +583,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t n
         : "memory");
 }
 
+// The two halves of an f16x2 in fp32 (exact).
+__device__ __forceinline__ float2 f16_pair(uint32_t x) {
+    float2 r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t"
+        "cvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "r"(x));
+    return r;
+}
+
 // 1 / s of a sum of weights, or 0 without any; a NaN stays one.
 __device__ __forceinline__ float q4_over(float s) { return s > 0.0f ? 1.0f / s : s == s ? 0.0f : s; }
 
